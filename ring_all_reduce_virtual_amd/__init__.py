@@ -20,6 +20,12 @@ need a power-of-two rank count and return the same bits); ``"select"`` picks
 ``"ring"`` otherwise, and returns the bits of the one it picks.  ``"tree"``
 is the binomial-tree all-gather (gather to rank 0, broadcast from it; the
 all-gather only).
+
+The tensor-parallel layer's operators (include/vrc_ops.h, ``libvrc_ops.so``)
+stand beside them: dropout inside the collectives (``vrc_allreduce_dropout``,
+``vrc_reduce_scatter_dropout``, ``vrc_all_gather_dropout``) and microscaled
+4-bit matrices (``vrc_mx4_quantize``, ``vrc_mx4_dequantize``,
+``vrc_mx4_all_gather``, ``vrc_mx4_matmul``).
 """
 from __future__ import annotations
 
@@ -45,10 +51,10 @@ HD_MODES = ("hd", "hd_order")  # halving-doubling; nranks must be a power of two
 
 
 class VrcError(RuntimeError):
-    def __init__(self, status: int, where: str):
+    def __init__(self, status: int, where: str, hip_error: int | None = None):
         msg = _lib.vrc_status_string(status).decode()
         if status == VRC_ERR_HIP:
-            msg += f" (hipError {_lib.vrc_last_hip_error()})"
+            msg += f" (hipError {_lib.vrc_last_hip_error() if hip_error is None else hip_error})"
         super().__init__(f"{where}: {msg}")
         self.status = status
 
@@ -436,3 +442,8 @@ __all__ = [
     "GATHER_ONLY_MODES", "RING_MODES", "HD_MODES", "VRC_OK",
     "VRC_ERR_INVALID_ARG", "VRC_ERR_UNSUPPORTED", "VRC_ERR_ALIAS", "VRC_ERR_HIP", "MAX_RANKS",
 ]
+
+from .ops import *  # noqa: E402,F401,F403  (needs the names above)
+from .ops import __all__ as _ops_all  # noqa: E402
+
+__all__ += _ops_all

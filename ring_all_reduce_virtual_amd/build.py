@@ -1,4 +1,4 @@
-"""Build the HIP library (libvrc.so) for gfx950 with hipcc, in-tree."""
+"""Build the HIP libraries (libvrc.so, libvrc_ops.so) for gfx950 with hipcc, in-tree."""
 from __future__ import annotations
 
 import os
@@ -10,10 +10,16 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libvrc.so")
+LIB_OPS = os.path.join(PKG, "libvrc_ops.so")
 # One translation unit per element type holds that type's kernels; vrc_api.hip
 # holds the C ABI.  They compile in parallel.
 SOURCES = [os.path.join(CSRC, f) for f in
            ("vrc_type_bf16.hip", "vrc_type_f16.hip", "vrc_type_f32.hip", "vrc_type_i32.hip", "vrc_api.hip")]
+# The tensor-parallel layer's operators (include/vrc_ops.h) are a library of
+# their own: libvrc.so's kernels only stream through registers, and its tests
+# pin that; these use LDS and the matrix cores.
+SOURCES_OPS = [os.path.join(CSRC, f) for f in
+               ("vrc_dropout.hip", "vrc_mx4_matmul.hip", "vrc_mx4.hip", "vrc_ops_api.hip")]
 OBJDIR = os.path.join(PKG, "_build")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -67,13 +73,15 @@ def build_cvt_check(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False, jobs: int = 0) -> str:
-    """Compile every source to an object (in parallel) and link libvrc.so."""
+    """Compile every source to an object (in parallel), link libvrc.so and
+    libvrc_ops.so, and return libvrc.so's path."""
     os.makedirs(OBJDIR, exist_ok=True)
-    jobs = jobs or min(len(SOURCES), os.cpu_count() or 1, 16)
-    objs, pending = [], []
-    for src in SOURCES:
+    sources = SOURCES + SOURCES_OPS
+    jobs = jobs or min(len(sources), os.cpu_count() or 1, 16)
+    objs, pending = {}, []
+    for src in sources:
         obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
-        objs.append(obj)
+        objs[src] = obj
         cmd = [HIPCC, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", "-o", obj, src]
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -89,12 +97,13 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
             failed = cmd
     if failed is not None:
         raise subprocess.CalledProcessError(1, failed)
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    for lib, srcs in ((LIB, SOURCES), (LIB_OPS, SOURCES_OPS)):
+        tmp = lib + ".tmp"
+        cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *(objs[s] for s in srcs)]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, lib)
     return LIB
 
 

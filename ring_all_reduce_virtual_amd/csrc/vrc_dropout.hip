@@ -1,0 +1,488 @@
+// vrc_dropout.hip -- dropout inside the collectives: the all-reduce and the
+// reduce-scatter with a residual, and the masked all-gather that is the
+// reduce-scatter's gradient.
+//
+// y = res + mask * scale * (x_0 + x_1 + ... ) per element, in fp32, rounded
+// once.  The mask comes from Philox-4x32-10 by the element's index, so no call
+// stores or reads it: a kernel moves the collective's bytes and the residual's.
+// They are streams, bounded by memory; the generator's integer
+// multiplications (20 of 32 x 32 bits for four elements) run beside them.
+#include <hip/hip_runtime.h>
+
+#include "vrc_ops_host.hpp"
+
+namespace vrc {
+namespace {
+
+using host::MaskArgs;
+
+// One Philox-4x32 bijection of ten rounds: counter (block, offset), key seed.
+__device__ __forceinline__ void philox(uint64_t block, uint64_t offset, uint64_t seed, uint32_t w[4])
+{
+    uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32);
+    uint32_t c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; r++) {
+        const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+        c1 = (uint32_t)p1;
+        c3 = (uint32_t)p0;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    w[0] = c0;
+    w[1] = c1;
+    w[2] = c2;
+    w[3] = c3;
+}
+
+struct Mask {
+    uint64_t seed, offset;
+    float scale;
+    uint32_t thr, kind;
+
+    __device__ explicit Mask(const MaskArgs& a)
+        : seed(a.seed), offset(a.offset), scale(a.scale), thr(a.thr), kind(a.kind)
+    {
+        if (a.offset_dev) offset += *(global_ptr<const uint64_t>)a.offset_dev;
+    }
+
+    // Bit j: element 4 * block + j is kept.
+    __device__ __forceinline__ uint32_t keep4(uint64_t block) const
+    {
+        uint32_t w[4];
+        philox(block, offset, seed, w);
+        return (uint32_t)(w[0] >= thr) | (uint32_t)(w[1] >= thr) << 1 | (uint32_t)(w[2] >= thr) << 2 |
+               (uint32_t)(w[3] >= thr) << 3;
+    }
+
+    // Bit j: element i + j is kept, j < V.  A vector whose first index is no
+    // multiple of four reaches into one block more.
+    template <int V>
+    __device__ __forceinline__ uint32_t keep(uint64_t i) const
+    {
+        if (kind != 1) return kind == 0 ? ~0u : 0u;
+        const uint64_t b = i >> 2;
+        const uint32_t ph = (uint32_t)i & 3;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int j = 0; j < (V + 3) / 4; j++) bits |= keep4(b + j) << (4 * j);
+        if constexpr (V > 1) {
+            if (ph) bits |= keep4(b + V / 4) << V;
+        }
+        return bits >> ph;
+    }
+
+    // mask * scale * a, with +0 for a dropped element.
+    __device__ __forceinline__ float apply(float a, uint32_t bits, int j) const
+    {
+        return (bits >> j & 1u) ? a * scale : 0.0f;
+    }
+};
+
+// The N inputs' vectors, folded in rank order in fp32.
+template <class T, int N>
+__device__ __forceinline__ void fold_f32(const u32x4* in, float* acc)
+{
+    T::unpack(in[0], acc);
+#pragma unroll
+    for (int r = 1; r < N; r++) {
+        float x[T::VEC];
+        T::unpack(in[r], x);
+#pragma unroll
+        for (int i = 0; i < T::VEC; i++) acc[i] += x[i];
+    }
+}
+
+template <class T>
+__device__ __forceinline__ u32x4 add_residual(const float* acc, u32x4 res)
+{
+    float x[T::VEC];
+    T::unpack(res, x);
+#pragma unroll
+    for (int i = 0; i < T::VEC; i++) x[i] = acc[i] + x[i];
+    return T::pack(x);
+}
+
+// ---------------------------------------------------------------------------
+// All-reduce.  One-wave workgroups; a wave takes U consecutive 1 KiB tiles of
+// every buffer an iteration with all its loads in flight.  A lane reads its
+// elements of every input and residual before it writes any output, so an
+// output may be its own input or residual.
+// RES: 0 none, 1 one residual for all ranks, 2 one for each.
+// ---------------------------------------------------------------------------
+struct DropArArgs {
+    const char* src[kMaxRanks];
+    const char* res[kMaxRanks];
+    char* dst[kMaxRanks];
+    RowSplit g;
+    MaskArgs m;
+};
+
+template <class T, int N, int RES, int U>
+__global__ __launch_bounds__(64) void k_dropout_allreduce(DropArArgs a)
+{
+    constexpr uint64_t W = 64, E = T::ESZ;
+    constexpr int NR = RES == 2 ? N : RES;
+    const Mask mask(a.m);
+    const uint64_t body = a.g.head * E, nv = a.g.nvb, lane = threadIdx.x;
+    const auto tile = [&](uint64_t v, int groups) {
+        u32x4 in[U][N], res[U][NR ? NR : 1];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (u >= groups) break;
+#pragma unroll
+            for (int r = 0; r < N; r++) in[u][r] = ld16<true>(a.src[r] + body + (v + u * W) * 16);
+#pragma unroll
+            for (int r = 0; r < NR; r++) res[u][r] = ld16<true>(a.res[r] + body + (v + u * W) * 16);
+        }
+        issue_loads_first();
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (u >= groups) break;
+            const uint64_t at = v + u * W;
+            float acc[T::VEC];
+            fold_f32<T, N>(in[u], acc);
+            const uint32_t bits = mask.keep<T::VEC>(a.g.head + at * T::VEC);
+#pragma unroll
+            for (int i = 0; i < T::VEC; i++) acc[i] = mask.apply(acc[i], bits, i);
+            u32x4 out = RES == 0 ? T::pack(acc) : u32x4{};
+            if constexpr (RES == 1) out = add_residual<T>(acc, res[u][0]);
+#pragma unroll
+            for (int r = 0; r < N; r++) {
+                if constexpr (RES == 2) out = add_residual<T>(acc, res[u][r]);
+                st16<true>(a.dst[r] + body + at * 16, out);
+            }
+        }
+    };
+    const uint64_t groups = nv / W / U;
+    for (uint64_t g = blockIdx.x; g < groups; g += gridDim.x) tile(g * U * W + lane, U);
+    for (uint64_t v = (groups * U + blockIdx.x) * W + lane; v < nv; v += (uint64_t)gridDim.x * W) tile(v, 1);
+
+    const uint64_t ns = a.g.head + a.g.tail;
+    for (uint64_t k = blockIdx.x * W + lane; k < ns; k += (uint64_t)gridDim.x * W) {
+        const uint64_t i = k < a.g.head ? k : a.g.nvb * T::VEC + k;
+        float acc = T::widen(load_s<T>(a.src[0] + i * E));
+#pragma unroll
+        for (int r = 1; r < N; r++) acc += T::widen(load_s<T>(a.src[r] + i * E));
+        acc = mask.apply(acc, mask.keep<1>(i), 0);
+        float x[NR ? NR : 1];
+#pragma unroll
+        for (int r = 0; r < NR; r++) x[r] = T::widen(load_s<T>(a.res[r] + i * E));
+#pragma unroll
+        for (int r = 0; r < N; r++)
+            store_s<T>(a.dst[r] + i * E, T::narrow(RES == 0 ? acc : acc + x[RES == 2 ? r : 0]));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Chunks of the whole tensor: chunk c is `rows` rows of g[c]'s width at element
+// off[c] of the tensor, its rows `stride` elements apart there and packed in
+// the rank's own buffer.
+// ---------------------------------------------------------------------------
+struct ChunkArgs {
+    uint64_t off[kMaxRanks];
+    uint64_t width[kMaxRanks];
+    RowSplit g[kMaxRanks];
+    FastDiv by_nvb[kMaxRanks];
+    uint64_t rows, stride;
+    uint64_t tiles;  // wave tiles per chunk (the largest chunk's)
+    int n;
+};
+
+// Wave tile t: chunk and tile within it.  A flat split (rows == 1) walks the
+// tensor in address order; a split by columns takes the chunks in turn, so that
+// the workgroups at work read neighbouring columns of the same rows.
+__device__ __forceinline__ void tile_chunk(const ChunkArgs& a, uint64_t t, int& c, uint64_t& j)
+{
+    if (a.rows == 1) {
+        c = (int)(t / a.tiles);
+        j = t - (uint64_t)c * a.tiles;
+    } else {
+        j = t / (uint64_t)a.n;
+        c = (int)(t - j * (uint64_t)a.n);
+    }
+    c = __builtin_amdgcn_readfirstlane(c);
+}
+
+// Vector v of chunk c: its row and first column.
+template <class T>
+__device__ __forceinline__ void vector_place(const ChunkArgs& a, int c, uint64_t v, uint64_t& row, uint64_t& col)
+{
+    const RowSplit& g = a.g[c];
+    row = 0;
+    if (a.rows != 1) row = (a.rows * g.nvb) >> 31 ? v / g.nvb : a.by_nvb[c].div((uint32_t)v);
+    col = g.head + (v - row * g.nvb) * T::VEC;
+}
+
+struct DropRsArgs {
+    const char* src[kMaxRanks];
+    const char* res[kMaxRanks];
+    char* dst[kMaxRanks];
+    ChunkArgs ch;
+    MaskArgs m;
+};
+
+template <class T, int N, bool RES>
+__global__ __launch_bounds__(64) void k_dropout_reduce_scatter(DropRsArgs a)
+{
+    constexpr uint64_t W = 64, E = T::ESZ;
+    const Mask mask(a.m);
+    const uint64_t lane = threadIdx.x;
+    const ChunkArgs& ch = a.ch;
+    for (uint64_t t = blockIdx.x; t < ch.tiles * N; t += gridDim.x) {
+        int c;
+        uint64_t j;
+        tile_chunk(ch, t, c, j);
+        const uint64_t v = j * W + lane;
+        if (v >= ch.rows * ch.g[c].nvb) continue;
+        uint64_t row, col;
+        vector_place<T>(ch, c, v, row, col);
+        const uint64_t i = ch.off[c] + row * ch.stride + col;
+        const uint64_t o = (row * ch.width[c] + col) * E;
+        u32x4 in[N], res = {};
+#pragma unroll
+        for (int r = 0; r < N; r++) in[r] = ld16<true>(a.src[r] + i * E);
+        if constexpr (RES) res = ld16<true>(a.res[c] + o);
+        issue_loads_first();
+        float acc[T::VEC];
+        fold_f32<T, N>(in, acc);
+        const uint32_t bits = mask.keep<T::VEC>(i);
+#pragma unroll
+        for (int k = 0; k < T::VEC; k++) acc[k] = mask.apply(acc[k], bits, k);
+        st16<true>(a.dst[c] + o, RES ? add_residual<T>(acc, res) : T::pack(acc));
+    }
+    for (int c = 0; c < N; c++) {
+        const RowSplit& g = ch.g[c];
+        const uint64_t ns = ch.rows * (g.head + g.tail);
+        for (uint64_t k = blockIdx.x * W + lane; k < ns; k += (uint64_t)gridDim.x * W) {
+            uint64_t row, col;
+            scalar_slot(k, g, T::VEC, row, col);
+            const uint64_t i = ch.off[c] + row * ch.stride + col;
+            const uint64_t o = (row * ch.width[c] + col) * E;
+            float acc = T::widen(load_s<T>(a.src[0] + i * E));
+#pragma unroll
+            for (int r = 1; r < N; r++) acc += T::widen(load_s<T>(a.src[r] + i * E));
+            acc = mask.apply(acc, mask.keep<1>(i), 0);
+            if constexpr (RES) acc += T::widen(load_s<T>(a.res[c] + o));
+            store_s<T>(a.dst[c] + o, T::narrow(acc));
+        }
+    }
+}
+
+struct DropAgArgs {
+    const char* src[kMaxRanks];
+    char* dst[kMaxRanks];
+    ChunkArgs ch;
+    MaskArgs m;
+};
+
+template <class T>
+__global__ __launch_bounds__(64) void k_dropout_all_gather(DropAgArgs a)
+{
+    constexpr uint64_t W = 64, E = T::ESZ;
+    const Mask mask(a.m);
+    const uint64_t lane = threadIdx.x;
+    const ChunkArgs& ch = a.ch;
+    for (uint64_t t = blockIdx.x; t < ch.tiles * (uint64_t)ch.n; t += gridDim.x) {
+        int c;
+        uint64_t j;
+        tile_chunk(ch, t, c, j);
+        const uint64_t v = j * W + lane;
+        if (v >= ch.rows * ch.g[c].nvb) continue;
+        uint64_t row, col;
+        vector_place<T>(ch, c, v, row, col);
+        const uint64_t i = ch.off[c] + row * ch.stride + col;
+        const u32x4 in = ld16<true>(a.src[c] + (row * ch.width[c] + col) * E);
+        const uint32_t bits = mask.keep<T::VEC>(i);
+        float x[T::VEC];
+        T::unpack(in, x);
+#pragma unroll
+        for (int k = 0; k < T::VEC; k++) x[k] = mask.apply(x[k], bits, k);
+        const u32x4 out = T::pack(x);
+        for (int r = 0; r < ch.n; r++) st16<true>(a.dst[r] + i * E, out);
+    }
+    for (int c = 0; c < ch.n; c++) {
+        const RowSplit& g = ch.g[c];
+        const uint64_t ns = ch.rows * (g.head + g.tail);
+        for (uint64_t k = blockIdx.x * W + lane; k < ns; k += (uint64_t)gridDim.x * W) {
+            uint64_t row, col;
+            scalar_slot(k, g, T::VEC, row, col);
+            const uint64_t i = ch.off[c] + row * ch.stride + col;
+            const float x = T::widen(load_s<T>(a.src[c] + (row * ch.width[c] + col) * E));
+            const typename T::S s = T::narrow(mask.apply(x, mask.keep<1>(i), 0));
+            for (int r = 0; r < ch.n; r++) store_s<T>(a.dst[r] + i * E, s);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+using namespace host;
+
+// Workgroups: one per wave tile, up to `per_cu` per CU; tails and heads need
+// at least one.
+unsigned wave_grid(uint64_t tiles, int cus, int per_cu)
+{
+    const uint64_t cap = (uint64_t)cus * (uint64_t)per_cu;
+    const uint64_t g = tiles < cap ? tiles : cap;
+    return (unsigned)(g < 1 ? 1 : g);
+}
+
+template <class T, int N, int RES>
+vrc_status_t launch_ar(const DropArArgs& a, int cus, hipStream_t st)
+{
+    const uint64_t tiles = (a.g.nvb + 63) / 64;
+    k_dropout_allreduce<T, N, RES, 1><<<wave_grid(tiles, cus, 8), 64, 0, st>>>(a);
+    return check_launch();
+}
+
+template <class T, int N>
+vrc_status_t launch_ar_res(const DropArArgs& a, int res, int cus, hipStream_t st)
+{
+    switch (res) {
+    case 0: return launch_ar<T, N, 0>(a, cus, st);
+    case 1: return launch_ar<T, N, 1>(a, cus, st);
+    }
+    return launch_ar<T, N, 2>(a, cus, st);
+}
+
+template <class T>
+vrc_status_t allreduce_typed(const char* const* x, const char* const* res, char* const* y, int n, uint64_t count,
+                             const MaskArgs& m, int cus, hipStream_t st)
+{
+    DropArArgs a = {};
+    int kind = res ? 1 : 0;
+    uintptr_t dst[kMaxRanks];
+    for (int r = 0; r < n; r++) {
+        a.src[r] = x[r];
+        a.dst[r] = y[r];
+        dst[r] = (uintptr_t)y[r];
+        if (res) {
+            a.res[r] = res[r];
+            if (res[r] != res[0]) kind = 2;
+        }
+    }
+    a.g = split_rows(write_ref(dst, n), count, T::ESZ);
+    a.m = m;
+    switch (n) {
+    case 1: return launch_ar_res<T, 1>(a, kind, cus, st);
+#define VRC_CASE(N) \
+    case N: return launch_ar_res<T, N>(a, kind, cus, st);
+        VRC_FOR_N(VRC_CASE)
+#undef VRC_CASE
+    }
+    return VRC_ERR_INVALID_ARG;
+}
+
+// The chunks of a tensor of `total` elements split over n ranks: flat for
+// outer == 1, by columns otherwise.  `ref` gives the address that chunk c's
+// vector grid follows.
+template <class T, class Ref>
+ChunkArgs make_chunks(int n, uint64_t total, uint64_t outer, Ref ref)
+{
+    ChunkArgs a = {};
+    a.n = n;
+    a.rows = outer;
+    a.stride = total / outer;
+    for (int c = 0; c < n; c++) {
+        if (outer == 1) {
+            chunk_range(total, n, c, &a.off[c], &a.width[c]);
+        } else {
+            a.width[c] = a.stride / (uint64_t)n;
+            a.off[c] = (uint64_t)c * a.width[c];
+        }
+        a.g[c] = split_rows(ref(c, a.off[c]), a.width[c], T::ESZ);
+        a.by_nvb[c] = FastDiv::of(a.g[c].nvb);
+        const uint64_t tiles = (a.rows * a.g[c].nvb + 63) / 64;
+        if (tiles > a.tiles) a.tiles = tiles;
+    }
+    return a;
+}
+
+template <class T>
+vrc_status_t reduce_scatter_typed(const char* const* x, const char* const* res, char* const* y, int n, uint64_t count,
+                                  uint64_t outer, const MaskArgs& m, int cus, hipStream_t st)
+{
+    DropRsArgs a = {};
+    for (int r = 0; r < n; r++) {
+        a.src[r] = x[r];
+        a.dst[r] = y[r];
+        a.res[r] = res ? res[r] : nullptr;
+    }
+    a.ch = make_chunks<T>(n, count, outer, [&](int c, uint64_t) { return (uintptr_t)y[c]; });
+    a.m = m;
+    const unsigned grid = wave_grid(a.ch.tiles * (uint64_t)n, cus, 8);
+    switch (n) {
+#define VRC_CASE(N)                                                                  \
+    case N:                                                                          \
+        if (res) k_dropout_reduce_scatter<T, N, true><<<grid, 64, 0, st>>>(a);       \
+        else k_dropout_reduce_scatter<T, N, false><<<grid, 64, 0, st>>>(a);          \
+        return check_launch();
+        VRC_CASE(1)
+        VRC_FOR_N(VRC_CASE)
+#undef VRC_CASE
+    }
+    return VRC_ERR_INVALID_ARG;
+}
+
+template <class T>
+vrc_status_t all_gather_typed(const char* const* x, char* const* y, int n, uint64_t total, uint64_t outer,
+                              const MaskArgs& m, int cus, hipStream_t st)
+{
+    DropAgArgs a = {};
+    uintptr_t dst[kMaxRanks];
+    for (int r = 0; r < n; r++) {
+        a.src[r] = x[r];
+        a.dst[r] = y[r];
+        dst[r] = (uintptr_t)y[r];
+    }
+    const uintptr_t at = write_ref(dst, n);
+    a.ch = make_chunks<T>(n, total, outer, [&](int, uint64_t off) { return at + off * T::ESZ; });
+    a.m = m;
+    k_dropout_all_gather<T><<<wave_grid(a.ch.tiles * (uint64_t)n, cus, 32), 64, 0, st>>>(a);
+    return check_launch();
+}
+
+}  // namespace
+
+namespace host {
+
+#define VRC_BY_TYPE(call)                      \
+    switch (dt) {                              \
+    case VRC_FP32: return call(F32);           \
+    case VRC_FP16: return call(F16);           \
+    case VRC_BF16: return call(BF16);          \
+    default: return VRC_ERR_UNSUPPORTED;       \
+    }
+
+vrc_status_t run_allreduce_dropout(const char* const* x, const char* const* res, char* const* y, int n, uint64_t count,
+                                   vrc_dtype_t dt, const MaskArgs& m, int cus, hipStream_t st)
+{
+#define VRC_CALL(T) allreduce_typed<T>(x, res, y, n, count, m, cus, st)
+    VRC_BY_TYPE(VRC_CALL)
+#undef VRC_CALL
+}
+
+vrc_status_t run_reduce_scatter_dropout(const char* const* x, const char* const* res, char* const* y, int n,
+                                        uint64_t count, uint64_t outer, vrc_dtype_t dt, const MaskArgs& m, int cus,
+                                        hipStream_t st)
+{
+#define VRC_CALL(T) reduce_scatter_typed<T>(x, res, y, n, count, outer, m, cus, st)
+    VRC_BY_TYPE(VRC_CALL)
+#undef VRC_CALL
+}
+
+vrc_status_t run_all_gather_dropout(const char* const* x, char* const* y, int n, uint64_t total, uint64_t outer,
+                                    vrc_dtype_t dt, const MaskArgs& m, int cus, hipStream_t st)
+{
+#define VRC_CALL(T) all_gather_typed<T>(x, y, n, total, outer, m, cus, st)
+    VRC_BY_TYPE(VRC_CALL)
+#undef VRC_CALL
+}
+
+}  // namespace host
+}  // namespace vrc

@@ -1,0 +1,476 @@
+// vrc_mx4.hip -- microscaled 4-bit blocks: quantisation along either axis, and
+// decoding (each rank's own matrix, or the gather of all of them).
+//
+// A block of 32 values shares 2^X, X = floor(log2 max|v|) - 2: the exponent
+// field of the largest magnitude less two, so no logarithm is taken.  v / 2^X is
+// exact (a power of two) and rounded to E2M1 by the target's conversions, which
+// equal the definition (nearest, ties to even, saturating at 6) on every finite
+// fp16 and bf16 value under every scale.  Both directions are streams: 2 or 4
+// bytes a value on one side, 17/32 on the other.
+#include <hip/hip_runtime.h>
+
+#include "vrc_ops_host.hpp"
+
+namespace vrc {
+namespace {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// Two values to two codes in byte SEL of `old`, two codes to two values.  `s` is
+// the scale's byte in a float's exponent field (byte 0, a zero there, stands for
+// 2^-127 to these conversions; byte 255 decodes to NaN).
+template <class T>
+struct Mx4;
+
+template <>
+struct Mx4<F32> {
+    template <int SEL>
+    __device__ static uint32_t encode(uint32_t old, uint32_t a, uint32_t b, float s)
+    {
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, __uint_as_float(a), __uint_as_float(b), s, SEL);
+    }
+};
+
+template <>
+struct Mx4<BF16> {
+    template <int SEL>
+    __device__ static uint32_t encode(uint32_t old, uint32_t pair, float s)
+    {
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2, pair), s, SEL);
+    }
+    template <int SEL>
+    __device__ static uint32_t decode(uint32_t codes, float s)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, SEL));
+    }
+};
+
+template <>
+struct Mx4<F16> {
+    template <int SEL>
+    __device__ static uint32_t encode(uint32_t old, uint32_t pair, float s)
+    {
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(f16x2, pair), s, SEL);
+    }
+    template <int SEL>
+    __device__ static uint32_t decode(uint32_t codes, float s)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, s, SEL));
+    }
+};
+
+constexpr uint32_t kNanScale = 255;
+
+// The scale byte of a block whose largest magnitude has the bits m (sign
+// cleared): the exponent as a float's, less two, at least 0; 255 where m is an
+// infinity's or a NaN's.
+template <class T>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t m)
+{
+    uint32_t e;
+    if constexpr (T::ESZ == 4) e = m >> 23;
+    else if constexpr (std::is_same<T, BF16>::value) e = m >> 7;
+    else e = m >= 0x7c00u ? 255u : __float_as_uint(F16::widen((uint16_t)m)) >> 23;
+    return e == 255u ? kNanScale : (e > 2u ? e - 2u : 0u);
+}
+
+__device__ __forceinline__ float scale_float(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    return __builtin_bit_cast(
+        uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+
+// The larger of x over a lane's quad.
+__device__ __forceinline__ uint32_t quad_max(uint32_t x)
+{
+    const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xf, 0xf, true);  // lanes 1 0 3 2
+    x = x > y ? x : y;
+    const uint32_t z = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xf, 0xf, true);  // lanes 2 3 0 1
+    return x > z ? x : z;
+}
+
+// Eight consecutive values as they are stored: ESZ * 8 bytes.
+template <class T>
+struct Eight {
+    static constexpr int D = T::ESZ * 2;  // dwords
+    uint32_t w[D];
+
+    __device__ __forceinline__ void load(const char* p)
+    {
+#pragma unroll
+        for (int i = 0; i < D / 4; i++) {
+            const u32x4 v = ld16<true>(p + 16 * i);
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+    }
+    // The first `left` of them, zero after.
+    __device__ __forceinline__ void load_part(const char* p, int left)
+    {
+#pragma unroll
+        for (int i = 0; i < D; i++) w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            if (i >= left) continue;
+            const uint32_t s = load_s<T>(p + i * T::ESZ);
+            if constexpr (T::ESZ == 4) w[i] = s;
+            else w[i / 2] |= s << (16 * (i & 1));
+        }
+    }
+    // Bits of the largest magnitude.
+    __device__ __forceinline__ uint32_t top() const
+    {
+        constexpr uint32_t ABS = T::ESZ == 4 ? 0x7fffffffu : 0x7fff7fffu;
+        uint32_t m = w[0] & ABS;
+#pragma unroll
+        for (int i = 1; i < D; i++) {
+            const uint32_t x = w[i] & ABS;
+            if constexpr (T::ESZ == 4) m = m > x ? m : x;
+            else m = max_u16x2(m, x);
+        }
+        if constexpr (T::ESZ == 2) m = (m >> 16) > (m & 0xffffu) ? m >> 16 : m & 0xffffu;
+        return m;
+    }
+    __device__ __forceinline__ uint32_t encode(float s) const
+    {
+        uint32_t c = 0;
+        if constexpr (T::ESZ == 4) {
+            c = Mx4<T>::template encode<0>(c, w[0], w[1], s);
+            c = Mx4<T>::template encode<1>(c, w[2], w[3], s);
+            c = Mx4<T>::template encode<2>(c, w[4], w[5], s);
+            c = Mx4<T>::template encode<3>(c, w[6], w[7], s);
+        } else {
+            c = Mx4<T>::template encode<0>(c, w[0], s);
+            c = Mx4<T>::template encode<1>(c, w[1], s);
+            c = Mx4<T>::template encode<2>(c, w[2], s);
+            c = Mx4<T>::template encode<3>(c, w[3], s);
+        }
+        return c;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Quantisation along the rows.  A quad of lanes has a block, eight values a
+// lane: 16-byte loads (two for fp32) and 4-byte stores, consecutive over the
+// wave, and the block's maximum in two lane exchanges.  A lane keeps U groups'
+// loads in flight.  blockIdx.y is the rank.
+// FLAT: cols is a multiple of 32, so block b starts at value 32 b.
+// ---------------------------------------------------------------------------
+struct QuantArgs {
+    const char* src[kMaxRanks];
+    char* codes[kMaxRanks];
+    char* scales[kMaxRanks];
+    uint64_t cols, kb;
+    uint64_t groups;  // rows * kb * 4
+    FastDiv by_kb;
+};
+
+template <class T, bool FLAT>
+__global__ __launch_bounds__(256) void k_mx4_quantize(QuantArgs a)
+{
+    constexpr int U = 4;
+    constexpr uint64_t E = T::ESZ;
+    const char* src = a.src[blockIdx.y];
+    const auto codes = (global_ptr<uint32_t>)a.codes[blockIdx.y];
+    const auto scales = (global_ptr<uint8_t>)a.scales[blockIdx.y];
+    const uint64_t step = (uint64_t)gridDim.x * 256 * U;
+    for (uint64_t g0 = (uint64_t)blockIdx.x * 256 * U + threadIdx.x; g0 < a.groups; g0 += step) {
+        Eight<T> x[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const uint64_t g = g0 + u * 256;
+            if (g >= a.groups) continue;
+            if constexpr (FLAT) {
+                x[u].load(src + g * 8 * E);
+            } else {
+                const uint64_t b = g >> 2;
+                const uint64_t row = (a.groups >> 33) ? b / a.kb : a.by_kb.div((uint32_t)b);
+                const uint64_t col = (b - row * a.kb) * 32 + (g & 3) * 8;
+                const int64_t left = (int64_t)a.cols - (int64_t)col;
+                const char* p = src + (row * a.cols + col) * E;
+                if (left >= 8) x[u].load(p);
+                else x[u].load_part(p, left > 0 ? (int)left : 0);
+            }
+        }
+        issue_loads_first();
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const uint64_t g = g0 + u * 256;
+            if (g >= a.groups) continue;
+            const uint32_t byte = scale_byte<T>(quad_max(x[u].top()));
+            codes[g] = byte == kNanScale ? 0u : x[u].encode(scale_float(byte));
+            if ((g & 3) == 0) scales[g >> 2] = (uint8_t)byte;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Quantisation down the columns, stored transposed.  A lane has one dword of
+// every row (two columns of a 16-bit type, one of fp32) and reads the block's 32
+// rows, each a consecutive run over the wave; the maximum needs no exchange.
+// A workgroup's four waves take the eight blocks of 256 rows, so each column's
+// 128 bytes of codes come from one workgroup and meet in its L2.
+// blockIdx.y is the rank.
+// ---------------------------------------------------------------------------
+struct QuantTArgs {
+    const char* src[kMaxRanks];
+    char* codes[kMaxRanks];
+    char* scales[kMaxRanks];
+    uint64_t rows, cols, kb;
+    uint32_t col_tiles;
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void k_mx4_quantize_t(QuantTArgs a)
+{
+    constexpr uint64_t E = T::ESZ;
+    constexpr int C = 4 / T::ESZ;  // columns per lane
+    const uint64_t ct = blockIdx.x % a.col_tiles, rt = blockIdx.x / a.col_tiles;
+    const uint64_t col = (ct * 64 + (threadIdx.x & 63)) * C;
+    if (col >= a.cols) return;
+    // The last lane of an odd count of 16-bit columns reads its column and the
+    // one before, and shifts; a single column is read by itself.
+    const bool whole = col + C <= a.cols;
+    const bool single = C == 2 && a.cols == 1;
+    const uint32_t shift = whole || single ? 0 : 16;
+    const char* src = a.src[blockIdx.y] + (shift ? col - 1 : col) * E;
+    const uint64_t row_bytes = a.cols * E;
+    for (uint32_t k = 0; k < 2; k++) {
+        const uint64_t b = rt * 8 + (threadIdx.x >> 6) + 4 * k;
+        if (b >= a.kb) return;
+        // Rows past the end read the last row again and count as zeros.
+        const uint64_t left = a.rows - b * 32;
+        const uint32_t last = left < 32 ? (uint32_t)left - 1 : 31;
+        const char* p = src + b * 32 * row_bytes;
+        uint32_t x[32];
+#pragma unroll
+        for (uint32_t i = 0; i < 32; i++) {
+            typedef uint32_t u32_any __attribute__((aligned(2)));
+            const char* at = p + (i < last ? i : last) * row_bytes;
+            if (single) x[i] = load_s<T>(at);
+            else x[i] = *(global_ptr<const u32_any>)at;
+        }
+        issue_loads_first();
+#pragma unroll
+        for (uint32_t i = 0; i < 32; i++) x[i] = i <= last ? x[i] >> shift : 0;
+        constexpr uint32_t ABS = C == 1 ? 0x7fffffffu : 0x7fff7fffu;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 32; i++) {
+            const uint32_t m = x[i] & ABS;
+            if constexpr (C == 1) top = top > m ? top : m;
+            else top = max_u16x2(top, m);
+        }
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            if (c > 0 && !whole) break;
+            const uint32_t byte = scale_byte<T>(C == 1 ? top : (c ? top >> 16 : top & 0xffffu));
+            const float s = scale_float(byte);
+            uint32_t w[4];
+#pragma unroll
+            for (int d = 0; d < 4; d++) {
+                uint32_t code = 0;
+                if constexpr (C == 1) {
+                    code = Mx4<T>::template encode<0>(code, x[8 * d], x[8 * d + 1], s);
+                    code = Mx4<T>::template encode<1>(code, x[8 * d + 2], x[8 * d + 3], s);
+                    code = Mx4<T>::template encode<2>(code, x[8 * d + 4], x[8 * d + 5], s);
+                    code = Mx4<T>::template encode<3>(code, x[8 * d + 6], x[8 * d + 7], s);
+                } else {
+                    // column c of two rows side by side
+                    const auto pair = [&](int i) {
+                        return c ? (x[i] >> 16) | (x[i + 1] & 0xffff0000u) : (x[i] & 0xffffu) | (x[i + 1] << 16);
+                    };
+                    code = Mx4<T>::template encode<0>(code, pair(8 * d), s);
+                    code = Mx4<T>::template encode<1>(code, pair(8 * d + 2), s);
+                    code = Mx4<T>::template encode<2>(code, pair(8 * d + 4), s);
+                    code = Mx4<T>::template encode<3>(code, pair(8 * d + 6), s);
+                }
+                w[d] = byte == kNanScale ? 0u : code;
+            }
+            const uint64_t at = (col + c) * a.kb + b;
+            *(global_ptr<u32x4>)(a.codes[blockIdx.y] + at * 16) = u32x4{w[0], w[1], w[2], w[3]};
+            *(global_ptr<uint8_t>)(a.scales[blockIdx.y] + at) = (uint8_t)byte;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Decoding.  A lane has eight codes (4 bytes in, 16 or 32 out), written to every
+// output.  blockIdx.y is the rank whose codes are read.
+// FLAT: cols is a multiple of 32 and rows are packed in the outputs.
+// ---------------------------------------------------------------------------
+struct DecodeArgs {
+    const char* codes[kMaxRanks];
+    const char* scales[kMaxRanks];
+    char* dst[kMaxRanks];
+    int n_out;  // outputs that every rank's values go to; 0: rank q's go to dst[q] alone
+    uint64_t cols, kb, groups, slab, stride;
+    FastDiv by_kb;
+};
+
+template <class T>
+__device__ __forceinline__ void decode8(uint32_t c, float s, uint32_t* w)
+{
+    if constexpr (T::ESZ == 4) {
+        const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
+        const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+        const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
+        const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+        const float v[8] = {a.x, a.y, b.x, b.y, d.x, d.y, e.x, e.y};
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = __float_as_uint(v[i]);
+    } else {
+        w[0] = Mx4<T>::template decode<0>(c, s);
+        w[1] = Mx4<T>::template decode<1>(c, s);
+        w[2] = Mx4<T>::template decode<2>(c, s);
+        w[3] = Mx4<T>::template decode<3>(c, s);
+    }
+}
+
+template <class T, bool FLAT>
+__global__ __launch_bounds__(256) void k_mx4_decode(DecodeArgs a)
+{
+    constexpr uint64_t E = T::ESZ;
+    constexpr int D = T::ESZ * 2;
+    const int q = blockIdx.y;
+    const auto codes = (global_ptr<const uint32_t>)a.codes[q];
+    const auto scales = (global_ptr<const uint8_t>)a.scales[q];
+    const int r0 = a.n_out ? 0 : q, r1 = a.n_out ? a.n_out : q + 1;
+    const uint64_t step = (uint64_t)gridDim.x * 256;
+    for (uint64_t g = (uint64_t)blockIdx.x * 256 + threadIdx.x; g < a.groups; g += step) {
+        uint32_t w[D];
+        decode8<T>(codes[g], scale_float(scales[g >> 2]), w);
+        uint64_t at = (uint64_t)q * a.slab;
+        int64_t left = 8;
+        if constexpr (FLAT) {
+            at += g * 8;
+        } else {
+            const uint64_t b = g >> 2;
+            const uint64_t row = (a.groups >> 33) ? b / a.kb : a.by_kb.div((uint32_t)b);
+            const uint64_t col = (b - row * a.kb) * 32 + (g & 3) * 8;
+            left = (int64_t)a.cols - (int64_t)col;
+            at += row * a.stride + col;
+        }
+        if (left >= 8) {
+            for (int r = r0; r < r1; r++)
+#pragma unroll
+                for (int i = 0; i < D / 4; i++)
+                    st16<true>(a.dst[r] + at * E + 16 * i, u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]});
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                if (i >= left) continue;
+                const uint32_t s = E == 4 ? w[i % D] : w[(i / 2) % D] >> (16 * (i & 1));
+                for (int r = r0; r < r1; r++) store_s<T>(a.dst[r] + (at + i) * E, (typename T::S)s);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+using namespace host;
+
+unsigned block_grid(uint64_t items, uint64_t per_block, int n, int cus, int per_cu)
+{
+    uint64_t want = (items + per_block - 1) / per_block;
+    uint64_t cap = (uint64_t)cus * (uint64_t)per_cu / (uint64_t)n;
+    if (cap < 1) cap = 1;
+    if (want > cap) want = cap;
+    return (unsigned)(want < 1 ? 1 : want);
+}
+
+template <class T>
+vrc_status_t quantize_typed(const char* const* x, char* const* codes, char* const* scales, int n, uint64_t rows,
+                            uint64_t cols, bool along_rows, int cus, hipStream_t st)
+{
+    if (along_rows) {
+        QuantTArgs a = {};
+        for (int r = 0; r < n; r++) {
+            a.src[r] = x[r];
+            a.codes[r] = codes[r];
+            a.scales[r] = scales[r];
+        }
+        a.rows = rows;
+        a.cols = cols;
+        a.kb = (rows + 31) / 32;
+        constexpr uint64_t wide = 64 * (4 / T::ESZ);
+        const uint64_t ct = (cols + wide - 1) / wide, rt = (a.kb + 7) / 8;
+        if (ct > 0x7fffffffull || ct * rt > 0x7fffffffull) return VRC_ERR_INVALID_ARG;
+        a.col_tiles = (uint32_t)ct;
+        k_mx4_quantize_t<T><<<dim3((unsigned)(ct * rt), (unsigned)n), 256, 0, st>>>(a);
+        return check_launch();
+    }
+    QuantArgs a = {};
+    for (int r = 0; r < n; r++) {
+        a.src[r] = x[r];
+        a.codes[r] = codes[r];
+        a.scales[r] = scales[r];
+    }
+    a.cols = cols;
+    a.kb = (cols + 31) / 32;
+    a.groups = rows * a.kb * 4;
+    a.by_kb = FastDiv::of(a.kb);
+    const dim3 grid(block_grid(a.groups, 1024, n, cus, 8), (unsigned)n);
+    if (cols % 32 == 0) k_mx4_quantize<T, true><<<grid, 256, 0, st>>>(a);
+    else k_mx4_quantize<T, false><<<grid, 256, 0, st>>>(a);
+    return check_launch();
+}
+
+template <class T>
+vrc_status_t decode_typed(const char* const* codes, const char* const* scales, char* const* y, int n, int n_out,
+                          uint64_t rows, uint64_t cols, uint64_t slab, uint64_t stride, int cus, hipStream_t st)
+{
+    DecodeArgs a = {};
+    for (int r = 0; r < n; r++) {
+        a.codes[r] = codes[r];
+        a.scales[r] = scales[r];
+        a.dst[r] = y[r];
+    }
+    a.n_out = n_out;
+    a.cols = cols;
+    a.kb = (cols + 31) / 32;
+    a.groups = rows * a.kb * 4;
+    a.slab = slab;
+    a.stride = stride;
+    a.by_kb = FastDiv::of(a.kb);
+    const dim3 grid(block_grid(a.groups, 256, n, cus, 32), (unsigned)n);
+    if (cols % 32 == 0 && stride == cols) k_mx4_decode<T, true><<<grid, 256, 0, st>>>(a);
+    else k_mx4_decode<T, false><<<grid, 256, 0, st>>>(a);
+    return check_launch();
+}
+
+}  // namespace
+
+namespace host {
+
+vrc_status_t run_mx4_quantize(const char* const* x, char* const* codes, char* const* scales, int n, uint64_t rows,
+                              uint64_t cols, vrc_dtype_t dt, bool along_rows, int cus, hipStream_t st)
+{
+    switch (dt) {
+    case VRC_FP32: return quantize_typed<F32>(x, codes, scales, n, rows, cols, along_rows, cus, st);
+    case VRC_FP16: return quantize_typed<F16>(x, codes, scales, n, rows, cols, along_rows, cus, st);
+    case VRC_BF16: return quantize_typed<BF16>(x, codes, scales, n, rows, cols, along_rows, cus, st);
+    default: return VRC_ERR_UNSUPPORTED;
+    }
+}
+
+vrc_status_t run_mx4_decode(const char* const* codes, const char* const* scales, char* const* y, int n, int n_out,
+                            uint64_t rows, uint64_t cols, uint64_t slab, uint64_t stride, vrc_dtype_t dt, int cus,
+                            hipStream_t st)
+{
+    switch (dt) {
+    case VRC_FP32: return decode_typed<F32>(codes, scales, y, n, n_out, rows, cols, slab, stride, cus, st);
+    case VRC_FP16: return decode_typed<F16>(codes, scales, y, n, n_out, rows, cols, slab, stride, cus, st);
+    case VRC_BF16: return decode_typed<BF16>(codes, scales, y, n, n_out, rows, cols, slab, stride, cus, st);
+    default: return VRC_ERR_UNSUPPORTED;
+    }
+}
+
+}  // namespace host
+}  // namespace vrc
