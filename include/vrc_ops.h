@@ -151,7 +151,7 @@ typedef enum {
  *   for VRC_MX4_SUM, over all ranks, and rounded once.  The order of the sum is
  *   fixed by the sizes, so equal calls give equal bits.
  *   kblocks == 0 gives zeros.  Outputs overlap no other buffer.
- *   m, n < 2^31 and kblocks < 2^26.
+ *   m, n < 2^31, kblocks < 2^20.
  * Gradients of recv = A B^T, with G the output's gradient: A's is G B, the product of
  * G quantised along its columns and B quantised VRC_MX4_ALONG_ROWS; B's is G^T A, of
  * G and A both quantised VRC_MX4_ALONG_ROWS.

@@ -264,7 +264,7 @@ vrc_status_t mx4_matmul_impl(const void* const* ac_, const void* const* as_, con
     vrc_status_t rc = check_call(n, 0, dtype);
     if (rc) return rc;
     if (join != VRC_MX4_SUM && join != VRC_MX4_EACH) return VRC_ERR_UNSUPPORTED;
-    if (m >= 1ull << 31 || cols >= 1ull << 31 || kblocks >= 1ull << 26 || m * cols > kMaxCount) return VRC_ERR_INVALID_ARG;
+    if (m >= 1ull << 31 || cols >= 1ull << 31 || kblocks >= 1ull << 20 || m * cols > kMaxCount) return VRC_ERR_INVALID_ARG;
     if (m == 0 || cols == 0) return VRC_OK;
     const char *ac[kMaxRanks] = {}, *as[kMaxRanks] = {}, *bc[kMaxRanks] = {}, *bs[kMaxRanks] = {};
     char* y[kMaxRanks];

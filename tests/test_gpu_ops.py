@@ -457,6 +457,22 @@ def test_mx4_matmul_many_ranks(vrc, n):
             assert (out[r] == 3.0).all(), "written outside"
 
 
+@pytest.mark.parametrize("join,n,m,nc,k", [("sum", 1, 4001, 4100, 200), ("sum", 2, 4096, 4096, 96), ("each", 4, 2050, 1999, 300)])
+def test_mx4_matmul_large_tiles(vrc, join, n, m, nc, k):
+    """Enough work for the largest tiles, ragged and whole."""
+    a, b = [random_mx4(m, k, r) for r in range(n)], [random_mx4(nc, k, 90 + r) for r in range(n)]
+    ops = [list(t) for t in zip(*a)] + [list(t) for t in zip(*b)]
+    for dtype in ("fp32", "bf16"):
+        say(f"mx4_matmul {join} n={n} m={m} n={nc} k={k} {dtype}")
+        got = vrc.vrc_mx4_matmul(*ops, dtype=DT[dtype], join=join)
+        for r in range(n):
+            y, mag = product(*[[t[r]] for t in ops]) if join == "each" else product(*ops)
+            check_product(got[r], y, mag, k * (n if join == "sum" else 1), dtype, f"rank {r}")
+            if join == "sum":
+                assert all(torch.equal(got[0], g) for g in got)
+                break
+
+
 def test_mx4_matmul_special_scales(vrc):
     """A NaN scale reaches its row's or column's results and no others; scales far from
     one another meet in fp32's range; kblocks = 0 gives zeros."""

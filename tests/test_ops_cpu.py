@@ -116,7 +116,7 @@ def test_mx4_refusals():
 
     assert mm(n=0) == mm(n=17) == mm(ac=None) == mm(as_=None) == mm(bc=None) == mm(bs=None) == vrc.VRC_ERR_INVALID_ARG
     assert mm(y=None) == mm(ac=arr(A + 4, 2)) == mm(bc=arr(B + 8, 2)) == vrc.VRC_ERR_INVALID_ARG
-    assert mm(m=1 << 31) == mm(nc=1 << 31) == mm(kb=1 << 26) == mm(m=1 << 30, nc=1 << 30) == vrc.VRC_ERR_INVALID_ARG
+    assert mm(m=1 << 31) == mm(nc=1 << 31) == mm(kb=1 << 20) == mm(m=1 << 30, nc=1 << 30) == vrc.VRC_ERR_INVALID_ARG
     assert mm(dt=vrc.VRC_INT32) == mm(join=2) == vrc.VRC_ERR_UNSUPPORTED
     assert mm(y=arr(A, 2)) == mm(y=arr(B + (1 << 28), 2)) == mm(y=ops._ptr_array([R, R + 64])) == vrc.VRC_ERR_ALIAS
     assert mm(m=0) == mm(nc=0) == vrc.VRC_OK
