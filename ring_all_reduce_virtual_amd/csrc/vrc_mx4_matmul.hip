@@ -9,7 +9,16 @@
 // The contraction is walked in tiles of eight blocks (256 codes, 128 bytes a
 // row) of one rank; a row's last tile may hold fewer, whose missing blocks count
 // as zero codes with scale 1.
+//
+// Measured on MI355X, random codes: 8 x (4096 x 8192 x 4096) summed, eight bf16
+// outputs, 540 us (4.07 PFLOP/s; 107 us of it are the 537 MB of stores at the end of
+// each tile); 8192 x 8192 x 8192 253 us (4.34).  The matrix instructions alone,
+// operands from LDS but nothing loaded, take 213 us: random operands hold the
+// clock down (205 us whole on zeros), and 41 us of either are tile starts and
+// ends.  1 x 8192 x 8 x 4096, a stream of 143 MB: 26 us, 5.5 TB/s.
 #include <hip/hip_runtime.h>
+
+#include <utility>
 
 #include "vrc_ops_host.hpp"
 
@@ -17,6 +26,7 @@ namespace vrc {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
@@ -33,6 +43,7 @@ struct MatmulArgs {
     uint32_t m, n, kb;
     int ranks;
     uint32_t tiles_m, tiles_n;
+    uint64_t sm, sn;  // strides of C's rows and columns (the few-rows kernel)
 };
 
 // acc += the 64 products per output of step S (blocks 2S and 2S + 1) of a tile;
@@ -54,7 +65,7 @@ __device__ __forceinline__ uint32_t step_scales(u32x2 bytes, uint32_t half)
 
 // A row's eight scale bytes of the tile at `p`, or the `left` that it has and 127
 // (scale 1) for the rest.
-__device__ __forceinline__ u32x2 load_scales(const char* p, uint32_t left)
+__device__ __forceinline__ u32x2 row_of_scales(const char* p, uint32_t left)
 {
     if (left >= kTileBlocks) return *(global_ptr<const u32x2_any>)p;
     uint64_t v = 0x7f7f7f7f7f7f7f7full;
@@ -80,160 +91,16 @@ struct Four {
     }
 };
 
-// ---------------------------------------------------------------------------
-// Tiled product.  A workgroup of WM x WN waves has a BM x BN tile of C, a wave MI
-// x NI matrix-instruction tiles of it.  Each tile of the contraction is brought
-// into LDS by direct loads (16 bytes a lane, no registers) while the one before is
-// multiplied.
-//
-// LDS holds a row's eight 16-byte blocks with block j at place j ^ (row / 2 mod
-// 8), so that the 32 rows that a matrix operand reads at one block spread
-// over all banks; the loads permute their global addresses within the row's
-// 128 bytes to that end, as a direct load writes consecutive lanes to consecutive
-// places.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t place(uint32_t row, uint32_t block) { return block ^ (row >> 1 & 7); }
-
-// Every wave's direct loads have landed (a barrier alone does not wait for
-// them), and every wave is done with the stage it read.
-__device__ __forceinline__ void stage_barrier()
+// A wave's results to its outputs: MI x NI matrix-instruction tiles at (row0, col0)
+// of C, 32 rows at a time through `own`, the wave's part of LDS, so that they leave
+// in 16-byte stores along the rows.  Row r's 16-byte piece c is at c ^ (r mod 8)
+// (mod 4 where a row has four), which spreads a column over the banks.
+template <class T, int MI, int NI>
+__device__ __forceinline__ void store_results(const MatmulArgs& a, const f32x16 (&acc)[MI][NI], char* own, uint32_t lane,
+                                              uint32_t row0, uint32_t col0, int dst0, int dst1)
 {
-    wait_vmem_below<0>();
-    __syncthreads();
-}
-
-template <int BM, int BN>
-struct Stage {
-    char codes[(BM + BN) * kTileBytes];  // A's rows, then B's
-    u32x2 scales[BM + BN];
-};
-
-template <class T, bool SUM, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void k_mx4_matmul_tiled(MatmulArgs a)
-{
-    constexpr int MI = BM / WM / 32, NI = BN / WN / 32, WAVES = WM * WN, THREADS = WAVES * 64;
-    constexpr int CHUNKS = (BM + BN) / 8;  // of eight rows: 1 KiB, one load of a wave
-    static_assert(CHUNKS % WAVES == 0 && THREADS == BM + BN && BM % 64 == 0, "loads are shared out evenly");
-    __shared__ __attribute__((aligned(16))) Stage<BM, BN> stage[2];
-
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t m0 = blockIdx.x % a.tiles_m * BM, n0 = blockIdx.x / a.tiles_m * BN;
-    const uint32_t ktiles = (a.kb + kTileBlocks - 1) / kTileBlocks;
-    const int q0 = SUM ? 0 : (int)blockIdx.y;
-    const uint32_t total = ktiles * (SUM ? (uint32_t)a.ranks : 1u);
-    const uint64_t row_bytes = (uint64_t)a.kb * 16;
-
-    // This lane's part of each of its wave's loads: a row's offset from the tile's
-    // first row (rows past the end read the last one again) and its block.
-    uint32_t off[CHUNKS / WAVES];
-#pragma unroll
-    for (int i = 0; i < CHUNKS / WAVES; i++) {
-        const uint32_t chunk = wave * (CHUNKS / WAVES) + i;
-        const bool isb = chunk >= BM / 8;
-        const uint32_t row = (isb ? chunk - BM / 8 : chunk) * 8 + lane / 8;
-        const uint32_t last = isb ? a.n - 1 - n0 : a.m - 1 - m0;
-        off[i] = (row < last ? row : last) * (uint32_t)row_bytes + place(row, lane & 7) * 16;
-    }
-    const uint32_t srow = tid < BM ? (tid < a.m - m0 ? m0 + tid : a.m - 1)
-                                   : (tid - BM < a.n - n0 ? n0 + tid - BM : a.n - 1);
-
-    // Tile t of the contraction into a stage.
-    const auto fetch_codes = [&](Stage<BM, BN>& s, int q, uint32_t kt) {
-        const auto pa = (global_ptr<const char>)a.ac[q] + m0 * row_bytes + (uint64_t)kt * kTileBytes;
-        const auto pb = (global_ptr<const char>)a.bc[q] + n0 * row_bytes + (uint64_t)kt * kTileBytes;
-        const uint32_t left = a.kb - kt * kTileBlocks;
-        if (left >= kTileBlocks) {
-#pragma unroll
-            for (int i = 0; i < CHUNKS / WAVES; i++) {
-                const uint32_t chunk = wave * (CHUNKS / WAVES) + i;
-                __builtin_amdgcn_global_load_lds(
-                    (global_ptr<const void>)((chunk >= BM / 8 ? pb : pa) + off[i]),
-                    (__attribute__((address_space(3))) void*)(s.codes + chunk * 1024), 16, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < CHUNKS / WAVES; i++) {
-                const uint32_t chunk = wave * (CHUNKS / WAVES) + i;
-                u32x4 v = {};
-                if (place(chunk * 8 + lane / 8, lane & 7) < left) v = *(global_ptr<const u32x4>)((chunk >= BM / 8 ? pb : pa) + off[i]);
-                *(u32x4*)(s.codes + chunk * 1024 + lane * 16) = v;
-            }
-        }
-    };
-    const auto fetch_scales = [&](int q, uint32_t kt) {
-        const char* p = wave < BM / 64 ? a.as[q] : a.bs[q];  // one array per wave
-        return load_scales(p + (uint64_t)srow * a.kb + kt * kTileBlocks, a.kb - kt * kTileBlocks);
-    };
-
-    f32x16 acc[MI][NI] = {};
-    const uint32_t wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN);
+    constexpr uint32_t PITCH = NI * 32 * T::ESZ, VECS = NI * 32 / T::VEC, MIX = VECS < 8 ? VECS - 1 : 7;
     const uint32_t r = lane & 31, half = lane >> 5;
-    const auto multiply = [&](const Stage<BM, BN>& s) {
-        uint32_t sa[MI], sb[NI];
-#pragma unroll
-        for (int i = 0; i < MI; i++) sa[i] = step_scales(s.scales[wm + i * 32 + r], half);
-#pragma unroll
-        for (int j = 0; j < NI; j++) sb[j] = step_scales(s.scales[BM + wn + j * 32 + r], half);
-        // The next step's operands are read while one is multiplied; the scheduling
-        // barriers keep the compiler from reading all four at once, which takes
-        // more registers than there are.
-        u32x4 x[2][MI], y[2][NI];
-        const auto read = [&](int k) {
-            const uint32_t at = place(r, 2 * k + half) * 16;
-#pragma unroll
-            for (int j = 0; j < NI; j++) y[k & 1][j] = *(const u32x4*)(s.codes + (BM + wn + j * 32 + r) * kTileBytes + at);
-#pragma unroll
-            for (int i = 0; i < MI; i++) x[k & 1][i] = *(const u32x4*)(s.codes + (wm + i * 32 + r) * kTileBytes + at);
-        };
-        const auto step = [&](auto S) {
-            constexpr int k = decltype(S)::value;
-            if constexpr (k < 3) read(k + 1);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < MI; i++)
-#pragma unroll
-                for (int j = 0; j < NI; j++) acc[i][j] = mfma<k>(y[k & 1][j], x[k & 1][i], acc[i][j], sb[j], sa[i]);
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        read(0);
-        step(std::integral_constant<int, 0>{});
-        step(std::integral_constant<int, 1>{});
-        step(std::integral_constant<int, 2>{});
-        step(std::integral_constant<int, 3>{});
-    };
-
-    int q = q0;
-    uint32_t kt = 0;
-    if (total) {
-        fetch_codes(stage[0], q, kt);
-        const u32x2 sc = fetch_scales(q, kt);
-        stage[0].scales[tid] = sc;
-    }
-    for (uint32_t t = 0; t < total; t++) {
-        stage_barrier();
-        const uint32_t cur = t & 1, next = cur ^ 1;
-        if (++kt == ktiles) {
-            kt = 0;
-            q++;
-        }
-        u32x2 sc = {};
-        if (t + 1 < total) {
-            fetch_codes(stage[next], q, kt);
-            sc = fetch_scales(q, kt);
-        }
-        multiply(stage[cur]);
-        stage[next].scales[tid] = sc;
-    }
-    stage_barrier();
-
-    // The wave's results, 32 rows at a time through its own part of LDS, so that
-    // they leave in 16-byte stores along the rows of C.
-    // Row r's 16-byte piece c is at c ^ (r mod 8), which spreads a column over the banks.
-    constexpr uint32_t PITCH = NI * 32 * T::ESZ;
-    static_assert(WAVES * 32 * PITCH <= sizeof(stage[0].codes), "the epilogue fits a stage");
-    char* own = stage[0].codes + wave * 32 * PITCH;
-    const uint32_t vecs = NI * 32 / T::VEC;  // per row
-    const int dst0 = SUM ? 0 : q0, dst1 = SUM ? a.ranks : q0 + 1;
 #pragma unroll
     for (int i = 0; i < MI; i++) {
 #pragma unroll
@@ -243,16 +110,16 @@ __global__ __launch_bounds__(WM * WN * 64) void k_mx4_matmul_tiled(MatmulArgs a)
                 const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
                 const Four<T> f(v);
                 if constexpr (T::ESZ == 4) {
-                    *(u32x4*)(own + r * PITCH + ((j * 8 + 2 * g + half) ^ (r & 7)) * 16) =
+                    *(u32x4*)(own + r * PITCH + ((j * 8 + 2 * g + half) ^ (r & MIX)) * 16) =
                         u32x4{f.w[0], f.w[1], f.w[2], f.w[3]};
                 } else {
-                    *(u32x2*)(own + r * PITCH + ((j * 4 + g) ^ (r & 7)) * 16 + half * 8) = u32x2{f.w[0], f.w[1]};
+                    *(u32x2*)(own + r * PITCH + ((j * 4 + g) ^ (r & MIX)) * 16 + half * 8) = u32x2{f.w[0], f.w[1]};
                 }
             }
         __builtin_amdgcn_wave_barrier();
-        for (uint32_t v = lane; v < 32 * vecs; v += 64) {
-            const uint32_t row = m0 + wm + i * 32 + v / vecs, c = v % vecs * T::VEC, col = n0 + wn + c;
-            const u32x4 x = *(const u32x4*)(own + v / vecs * PITCH + (v % vecs ^ (v / vecs & 7)) * 16);
+        for (uint32_t v = lane; v < 32 * VECS; v += 64) {
+            const uint32_t row = row0 + i * 32 + v / VECS, col = col0 + v % VECS * T::VEC;
+            const u32x4 x = *(const u32x4*)(own + v / VECS * PITCH + (v % VECS ^ (v / VECS & MIX)) * 16);
             if (row >= a.m || col >= a.n) continue;
             const uint64_t at = ((uint64_t)row * a.n + col) * T::ESZ;
             if (col + T::VEC <= a.n) {
@@ -272,75 +139,598 @@ __global__ __launch_bounds__(WM * WN * 64) void k_mx4_matmul_tiled(MatmulArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// Few rows of A: a stream of B.  A workgroup has 32 columns of C (rows of B) and
-// all of C's rows (MI x 32); its waves take the contraction's tiles in turn,
-// straight from memory into registers, the next tile's loads in flight while one is
-// multiplied, and the waves' sums meet in LDS, added in wave order.
+// Tiled product.  A workgroup of WM x WN waves has a BM x BN tile of C, a wave MI
+// x NI matrix-instruction tiles of it.  The contraction's tiles come into a ring of
+// S stages in LDS by direct loads (no registers), up to S - 1 ahead.
+//
+// LDS holds a row's eight 16-byte blocks with block j at place j ^ (row / 2 mod
+// 8), so that the rows that a matrix operand reads at one block spread over all
+// banks; the loads permute their global addresses within the row's 128 bytes to
+// that end, as a direct load writes consecutive lanes to consecutive places.
+//
+// A row's scale bytes are in a memory line of their own, and a line costs the CU's
+// cache as much as one of 128 bytes of codes, so where rows allow (EVEN: kb a
+// multiple of 16, 16-byte aligned arrays) they come 16 at a time in the same way,
+// with the first of each two tiles.  Else a lane reads a row's eight bytes a tile
+// ahead and writes them to LDS, and blocks past a row's end come from a constant,
+// zero codes, and have scale 1.
+//
+// The loop over the tiles has no branch in it.  Past the last tile it goes on
+// fetching one word of it that nobody reads, so every wave always has the same
+// number of loads under way, which is what its waits count; and with a branch the
+// compiler moves the matrix instructions behind it, all four steps' operands live.
 // ---------------------------------------------------------------------------
-template <int MI>
+__device__ const u32x4 kZeroCodes = {0, 0, 0, 0};
+
+__device__ __forceinline__ uint32_t place(uint32_t row, uint32_t block) { return block ^ (row >> 1 & 7); }
+
+// A barrier behind this wave's LDS reads and writes, with its direct loads left
+// under way (__syncthreads() may wait for them).
+__device__ __forceinline__ void lds_barrier()
+{
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+}
+
+// A ring of S tiles, A's rows and then B's in each.
+template <int ROWS, int S, bool EVEN>
+struct Ring {
+    char codes[S][ROWS * kTileBytes];
+    u32x2 scales[EVEN ? S / 2 + 1 : S][ROWS][EVEN ? 2 : 1];  // a row's of two tiles or one
+};
+
+// One X a lane, lane l's to place l after `to` (a byte fills a dword there).
+template <class X>
+__device__ __forceinline__ void load_to_lds(global_ptr<const char> from, X* to)
+{
+    const auto g = (global_ptr<const void>)from;
+    const auto l = (__attribute__((address_space(3))) void*)to;
+    if constexpr (sizeof(X) == 16) __builtin_amdgcn_global_load_lds(g, l, 16, 0, 0);
+    else if constexpr (sizeof(X) == 4) __builtin_amdgcn_global_load_lds(g, l, 4, 0, 0);
+    else __builtin_amdgcn_global_load_lds(g, l, 1, 0, 0);
+}
+
+// Workgroup b's tile.  Workgroups are handed to the 8 XCDs in turn; each XCD takes
+// a run of consecutive tiles, in groups of G rows of tiles walked column by
+// column, so that the 32 or 64 tiles it works on at once share their operands'
+// rows in its L2.
+template <uint32_t G>
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn)
+{
+    const uint32_t total = tiles_m * tiles_n, each = total / 8, more = total % 8, x = b % 8;
+    const uint32_t t = x * each + (x < more ? x : more) + b / 8;
+    const uint32_t group = t / (G * tiles_n), left = tiles_m - group * G, rows = left < G ? left : G;
+    const uint32_t i = t - group * G * tiles_n;
+    tm = group * G + i % rows;
+    tn = i / rows;
+}
+
+// `x`, whose origin the compiler is not to see: an address is then a uniform base
+// and a 32-bit lane offset, which a load takes as they are, instead of a 64-bit
+// address per lane and load kept in registers over the whole loop.
+__device__ __forceinline__ uint32_t opaque(uint32_t x)
+{
+    __asm__ volatile("" : "+v"(x));
+    return x;
+}
+
+template <class T, bool SUM, bool EVEN, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__(WM * WN * 64) void k_mx4_matmul_tiled(MatmulArgs a)
+{
+    constexpr int MI = BM / WM / 32, NI = BN / WN / 32, WAVES = WM * WN;
+    constexpr int CODE_LOADS = (BM + BN) / 8 / WAVES;                      // of eight rows: 1 KiB
+    constexpr int SCALE_LOADS = (BM + BN) / 64 / WAVES;  // a tile's (EVEN: two tiles'), of 64 rows
+    constexpr int PAIR = EVEN ? 2 : 1;                   // tiles that scales come for at once
+    constexpr int NB = EVEN ? S / 2 + 1 : S;             // scale buffers
+    // Loads of the W tiles after one, where that one is (EVEN) the second of its two or the first.
+    constexpr auto loads = [](int w, bool second) {
+        return w * CODE_LOADS + (EVEN ? (second ? (w + 1) / 2 : w / 2) : w) * SCALE_LOADS;
+    };
+    static_assert((BM + BN) % (64 * WAVES) == 0 && BM % 64 == 0 && S >= 2, "loads are shared out evenly");
+    static_assert(EVEN || (S == 2 && SCALE_LOADS == 1), "rows' scales pass through a lane's registers");
+    static_assert(loads(S - 1, true) < 64, "the waits count at most 63 loads");
+    __shared__ __attribute__((aligned(16))) Ring<BM + BN, S, EVEN> ring;
+
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    uint32_t tm, tn;
+    tile_of<8>(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
+    const uint32_t m0 = tm * BM, n0 = tn * BN;
+    const uint32_t ktiles = (a.kb + kTileBlocks - 1) / kTileBlocks;
+    const int q0 = SUM ? 0 : (int)blockIdx.y;
+    const uint32_t total = ktiles * (SUM ? (uint32_t)a.ranks : 1u);
+    const uint64_t row_bytes = (uint64_t)a.kb * 16;
+
+    // This lane's part of each of its wave's loads, from the tile's first row (rows
+    // past the end read the last one again).
+    uint32_t off[CODE_LOADS], soff[SCALE_LOADS];
+#pragma unroll
+    for (int i = 0; i < CODE_LOADS; i++) {
+        const uint32_t at = (wave * CODE_LOADS + i) * 8;
+        const uint32_t row = (at >= BM ? at - BM : at) + lane / 8, last = at >= BM ? a.n - 1 - n0 : a.m - 1 - m0;
+        off[i] = (row < last ? row : last) * (uint32_t)row_bytes + place(row, lane & 7) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < SCALE_LOADS; i++) {
+        const uint32_t at = (wave * SCALE_LOADS + i) * 64;
+        const uint32_t row = (at >= BM ? at - BM : at) + lane, last = at >= BM ? a.n - 1 - n0 : a.m - 1 - m0;
+        soff[i] = (row < last ? row : last) * a.kb;
+    }
+    int fq = q0;  // the next tile to fetch
+    uint32_t fkt = 0, fetched = 0, fstage = 0, fbuf = 0;
+    // A wave's loads are all of A's rows or all of B's, so it has one pair of arrays.
+    constexpr uint32_t A_WAVES = BM / 8 / CODE_LOADS;
+    static_assert(BM % (8 * CODE_LOADS) == 0, "a wave loads rows of one operand");
+    const bool isb = wave >= A_WAVES;
+    const uint64_t row0 = isb ? n0 : m0;
+    global_ptr<const char> pcodes = nullptr, pscales = nullptr;
+    uint32_t live = 0, left = 0;
+    const auto aim = [&] {  // at the next tile
+        live = fetched < total ? ~0u : 0u;
+        left = a.kb - fkt * kTileBlocks;
+        pcodes = (global_ptr<const char>)(isb ? a.bc[fq] : a.ac[fq]) + row0 * row_bytes + (uint64_t)fkt * kTileBytes;
+        pscales = (global_ptr<const char>)(isb ? a.bs[fq] : a.as[fq]) + row0 * a.kb +
+                  (EVEN ? fkt & ~1u : fkt) * kTileBlocks;  // past the end fkt may be odd
+    };
+    const auto load_codes = [&](int i) {
+        const uint32_t at = (wave * CODE_LOADS + i) * 8;
+        auto from = pcodes + opaque(off[i] & live);
+        if constexpr (!EVEN)
+            if ((place(at + lane / 8, lane & 7) & live) >= left) from = (global_ptr<const char>)&kZeroCodes;
+        load_to_lds(from, (u32x4*)(ring.codes[fstage] + at * kTileBytes));
+    };
+    const auto load_scales = [&](int i) {
+        const uint32_t at = (wave * SCALE_LOADS + i) * 64;
+        load_to_lds(pscales + opaque(soff[i] & live), (u32x4*)ring.scales[fbuf][at]);
+    };
+    // !EVEN: this lane's row's eight bytes, to be written with keep_scales().  They
+    // are read at most seven bytes early, where eight would end past the array (which
+    // holds eight or more).
+    uint64_t held = 0;
+    uint32_t held_skip = 0, held_left = 0;
+    const uint64_t array_end = (isb ? a.n : a.m) * (uint64_t)a.kb - 8;
+    const auto hold_scales = [&] {
+        const uint64_t want = row0 * a.kb + (soff[0] & live) + fkt * kTileBlocks, from = want < array_end ? want : array_end;
+        typedef uint64_t u64_any __attribute__((aligned(1)));
+        held = *(global_ptr<const u64_any>)((global_ptr<const char>)(isb ? a.bs[fq] : a.as[fq]) + from);
+        held_skip = (uint32_t)(want - from);
+        held_left = left < kTileBlocks ? left : kTileBlocks;
+    };
+    const auto keep_scales = [&](uint32_t to) {
+        const uint64_t ones = held_left == kTileBlocks ? 0 : 0x7f7f7f7f7f7f7f7full << (8 * held_left);
+        const uint64_t keep = held_left == kTileBlocks ? ~0ull : ~(~0ull << (8 * held_left));
+        const uint64_t v = (held >> (8 * held_skip) & keep) | ones;
+        ring.scales[to][tid][0] = u32x2{(uint32_t)v, (uint32_t)(v >> 32)};
+    };
+    const auto advance = [&](auto first) {
+        if constexpr (decltype(first)::value) fbuf = fbuf + 1 == NB ? 0 : fbuf + 1;
+        fstage = fstage + 1 == S ? 0 : fstage + 1;
+        fetched++;
+        const bool more = fetched < total, wrap = fkt + 1 == ktiles;
+        fq += more && wrap;
+        fkt = !more ? fkt : wrap ? 0 : fkt + 1;
+    };
+    const auto fetch = [&](auto first) {
+        aim();
+#pragma unroll
+        for (int i = 0; i < CODE_LOADS; i++) load_codes(i);
+        if constexpr (!EVEN) {
+            hold_scales();
+        } else if constexpr (decltype(first)::value) {
+#pragma unroll
+            for (int i = 0; i < SCALE_LOADS; i++) load_scales(i);
+        }
+        advance(first);
+    };
+
+    f32x16 acc[MI][NI] = {};
+    const uint32_t wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN);
+    const uint32_t r = lane & 31, half = lane >> 5;
+    // A step's operands and a tile's scales, one ahead of the matrix instructions.
+    u32x4 x[2][MI], y[2][NI];
+    uint32_t sa[MI], sb[NI];
+    const auto read = [&](uint32_t cur, int k) {
+        const char* codes = ring.codes[cur];
+        const uint32_t at = place(r, 2 * k + half) * 16;
+#pragma unroll
+        for (int j = 0; j < NI; j++) y[k & 1][j] = *(const u32x4*)(codes + (BM + wn + j * 32 + r) * kTileBytes + at);
+#pragma unroll
+        for (int i = 0; i < MI; i++) x[k & 1][i] = *(const u32x4*)(codes + (wm + i * 32 + r) * kTileBytes + at);
+    };
+    const auto row_scales = [&](uint32_t buf, uint32_t second, uint32_t row) {
+        return step_scales(ring.scales[buf][row][second], half);
+    };
+    const auto read_scales = [&](uint32_t buf, uint32_t second, uint32_t* ua, uint32_t* ub) {
+#pragma unroll
+        for (int i = 0; i < MI; i++) ua[i] = row_scales(buf, second, wm + i * 32 + r);
+#pragma unroll
+        for (int j = 0; j < NI; j++) ub[j] = row_scales(buf, second, BM + wn + j * 32 + r);
+    };
+    const auto step = [&](auto K) {
+        constexpr int k = decltype(K)::value;
+#pragma unroll
+        for (int i = 0; i < MI; i++)
+#pragma unroll
+            for (int j = 0; j < NI; j++) acc[i][j] = mfma<k>(y[k & 1][j], x[k & 1][i], acc[i][j], sb[j], sa[i]);
+    };
+    // The scheduling barriers keep a step's reads before the step that they are to
+    // run behind: left alone, the compiler reads all four steps at once, which takes
+    // more registers than there are.
+    const auto settle = [] { __builtin_amdgcn_sched_barrier(0); };
+
+    // One tile: its first three steps, then, between its last read and its last
+    // step, the next tile's: it has landed for every wave, this tile's stage is
+    // free, and the next tile's first operands are on their way while the last step
+    // runs.  `second`: the tile is (EVEN) the second of its two.
+    uint32_t cur = 0, buf = 0;
+    const auto first_steps = [&] {
+        read(cur, 1);
+        settle();
+        step(std::integral_constant<int, 0>{});
+        settle();
+        read(cur, 2);
+        settle();
+        step(std::integral_constant<int, 1>{});
+        settle();
+        read(cur, 3);
+        settle();
+        step(std::integral_constant<int, 2>{});
+        settle();
+    };
+    const auto tile = [&](auto second) {
+        constexpr bool SECOND = decltype(second)::value;
+        first_steps();
+        wait_vmem_below<loads(S - 2, !SECOND)>();
+        if constexpr (!EVEN) keep_scales(cur ^ 1);  // the next tile's
+        __syncthreads();
+        // the tile S after this one, of the same place in its pair where S is even
+        fetch(std::integral_constant<bool, !EVEN || SECOND == (S % 2 != 0)>{});
+        cur = cur + 1 == S ? 0 : cur + 1;
+        if (!EVEN || SECOND) buf = buf + 1 == NB ? 0 : buf + 1;
+        uint32_t ua[MI], ub[NI];
+        read_scales(buf, EVEN && !SECOND, ua, ub);
+        read(cur, 0);
+        settle();
+        step(std::integral_constant<int, 3>{});
+        settle();
+#pragma unroll
+        for (int i = 0; i < MI; i++) sa[i] = ua[i];
+#pragma unroll
+        for (int j = 0; j < NI; j++) sb[j] = ub[j];
+    };
+    if (total) {
+#pragma unroll
+        for (int t = 0; t < S; t++) {
+            if (t % PAIR == 0) fetch(std::true_type{});
+            else fetch(std::false_type{});
+            if (!EVEN && t == 0) keep_scales(0);
+        }
+        wait_vmem_below<loads(S - 1, false)>();
+        __syncthreads();
+        read_scales(0, 0, sa, sb);
+        read(0, 0);
+        if constexpr (EVEN) {
+            for (uint32_t t = 2; t < total; t += 2) {
+                tile(std::false_type{});
+                tile(std::true_type{});
+            }
+            tile(std::false_type{});
+        } else {
+            for (uint32_t t = 1; t < total; t++) tile(std::false_type{});
+        }
+        first_steps();
+        step(std::integral_constant<int, 3>{});
+        wait_vmem_below<0>();
+    }
+    __syncthreads();
+
+    static_assert(WAVES * 32 * NI * 32 * T::ESZ <= sizeof(ring.codes), "the results' way out fits the ring");
+    store_results<T, MI, NI>(a, acc, ring.codes[0] + wave * 32 * NI * 32 * T::ESZ, lane, m0 + wm, n0 + wn, SUM ? 0 : q0,
+                             SUM ? a.ranks : q0 + 1);
+}
+
+// ---------------------------------------------------------------------------
+// Tiled product, large: 256 x 256 tiles, eight waves of 128 x 64, every row's
+// blocks in whole groups of G tiles (kb a multiple of 8 G, 16-byte aligned
+// scales).
+//
+// The waves of each half of the workgroup, one per SIMD, take turns: while one
+// half multiplies a step (256 cycles of matrix instructions), the other reads its
+// next step's operands from LDS, and a barrier swaps them.  Two stages: the next
+// tile's loads go out between the matrix instructions of a tile's first two steps,
+// into the stage that both halves have left, and have the last two steps to
+// land.  Scales come a group of G tiles ahead, 8 G bytes of a row at once, and are
+// read from LDS two tiles at a time behind the steps of the second.
+// ---------------------------------------------------------------------------
+template <int G>
+struct TurnsLds {
+    char codes[2][512 * kTileBytes];
+    u32x4 scales[2][512][G / 2];  // of two tiles each
+};
+
+template <class T, bool SUM, int G>
+__global__ __launch_bounds__(512) void k_mx4_matmul_turns(MatmulArgs a)
+{
+    constexpr int BM = 256, BN = 256, MI = 4, NI = 2, WAVES = 8;
+    static_assert(G == 2 || G == 4, "scales of one or two pairs of tiles");
+    __shared__ __attribute__((aligned(16))) TurnsLds<G> lds;
+
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    uint32_t tm, tn;
+    tile_of<4>(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
+    const uint32_t m0 = tm * BM, n0 = tn * BN;
+    const uint32_t ktiles = a.kb / kTileBlocks;
+    const int q0 = SUM ? 0 : (int)blockIdx.y;
+    const uint32_t total = ktiles * (SUM ? (uint32_t)a.ranks : 1u);
+    const uint64_t row_bytes = (uint64_t)a.kb * 16;
+
+    // Waves 0-3 load A's rows and 4-7 B's, 64 rows each: eight loads of eight rows'
+    // codes a tile, G / 2 loads of scales a group.  Offsets are from the operand's
+    // first row of the tile; rows past the end read the last one again.
+    const bool isb = wave >= 4;
+    const uint64_t row0 = isb ? n0 : m0;
+    const uint32_t last = isb ? a.n - 1 - n0 : a.m - 1 - m0, wrow = (wave & 3) * 64;
+    uint32_t off[8], soff[G / 2];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const uint32_t row = wrow + i * 8 + lane / 8;
+        off[i] = (row < last ? row : last) * (uint32_t)row_bytes + place(row, lane & 7) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < G / 2; i++) {
+        constexpr uint32_t L = G / 2;  // lanes of a row
+        const uint32_t row = wrow + (i * 64 + lane) / L;
+        soff[i] = (row < last ? row : last) * a.kb + lane % L * 16;
+    }
+
+    // The tile that is fetched next, and the group of scales after it.
+    int fq = q0;
+    uint32_t fkt = 0, fetched = 0, live = 0, slive = 0;
+    global_ptr<const char> pcodes = nullptr, pscales = nullptr;
+    const auto aim = [&] {
+        live = fetched < total ? ~0u : 0u;
+        pcodes = (global_ptr<const char>)(isb ? a.bc[fq] : a.ac[fq]) + row0 * row_bytes + (uint64_t)fkt * kTileBytes;
+    };
+    const auto aim_scales = [&](int q, uint32_t kt, bool more) {
+        slive = more ? ~0u : 0u;
+        pscales = (global_ptr<const char>)(isb ? a.bs[q] : a.as[q]) + row0 * a.kb + kt * kTileBlocks;
+    };
+    const auto load_codes = [&](uint32_t stage, int i) {
+        load_to_lds(pcodes + opaque(off[i] & live), (u32x4*)(lds.codes[stage] + ((isb ? BM : 0) + wrow + i * 8) * kTileBytes));
+    };
+    const auto load_scales = [&](uint32_t buf, int i) {
+        load_to_lds(pscales + opaque(soff[i] & slive), &lds.scales[buf][(isb ? BM : 0) + wrow][0] + i * 64);
+    };
+    const auto advance = [&] {
+        fetched++;
+        const bool more = fetched < total, wrap = fkt + 1 == ktiles;
+        fq += more && wrap;
+        fkt = !more ? fkt : wrap ? 0 : fkt + 1;
+    };
+
+    f32x16 acc[MI][NI] = {};
+    const uint32_t wm = wave % 2 * 128, wn = wave / 2 * 64;
+    const uint32_t r = lane & 31, half = lane >> 5;
+    u32x4 x[MI], y[NI];
+    uint32_t sa[2][MI], sb[2][NI];  // of the pair of tiles at work
+    uint32_t ta[2][MI], tb[2][NI];  // of the next
+    const auto read_scales = [&](uint32_t buf, int pair, int i) {  // rows' tile i of six: A's four, B's two
+        const u32x4 v = lds.scales[buf][i < MI ? wm + i * 32 + r : BM + wn + (i - MI) * 32 + r][pair];
+        const uint32_t u0 = step_scales(u32x2{v.x, v.y}, half), u1 = step_scales(u32x2{v.z, v.w}, half);
+        if (i < MI) { ta[0][i] = u0; ta[1][i] = u1; }
+        else { tb[0][i - MI] = u0; tb[1][i - MI] = u1; }
+    };
+    const auto take_scales = [&] {
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+#pragma unroll
+            for (int i = 0; i < MI; i++) sa[t][i] = ta[t][i];
+#pragma unroll
+            for (int j = 0; j < NI; j++) sb[t][j] = tb[t][j];
+        }
+    };
+    const auto settle = [] { __builtin_amdgcn_sched_barrier(0); };
+    const auto meet = [&] {
+        settle();
+        lds_barrier();
+        settle();
+    };
+
+    uint32_t buf = 0;
+    // Step K of tile g of a group (stage g mod 2).
+    const auto turn = [&](auto K, auto tile) {
+        constexpr int k = decltype(K)::value, g = decltype(tile)::value, stage = g & 1;
+        const char* codes = lds.codes[stage];
+        const uint32_t at = place(r, 2 * k + half) * 16;
+#pragma unroll
+        for (int j = 0; j < NI; j++) y[j] = *(const u32x4*)(codes + (BM + wn + j * 32 + r) * kTileBytes + at);
+#pragma unroll
+        for (int i = 0; i < MI; i++) x[i] = *(const u32x4*)(codes + (wm + i * 32 + r) * kTileBytes + at);
+        if constexpr (g % 2 == 1 && k > 0) {
+            read_scales(g == G - 1 ? buf ^ 1 : buf, g == G - 1 ? 0 : g / 2 + 1, 2 * k - 2);
+            read_scales(g == G - 1 ? buf ^ 1 : buf, g == G - 1 ? 0 : g / 2 + 1, 2 * k - 1);
+        }
+        if constexpr (k == 0) {
+            aim();
+            if constexpr (g == 0) {
+                // the group after this one: G - 1 tiles after the tile that is fetched next
+                const uint32_t kt = fkt + (G - 1);
+                const bool more = fetched + (G - 1) < total, wrap = kt == ktiles;
+                aim_scales(fq + (more && wrap), !more || wrap ? 0 : kt, more);
+            }
+        }
+        if constexpr (k == 3) {
+            advance();
+            wait_vmem_below<0>();
+        }
+        meet();
+        __builtin_amdgcn_s_setprio(1);
+        if constexpr (k == 0 && g == 0)
+#pragma unroll
+            for (int i = 0; i < G / 2; i++) load_scales(buf ^ 1, i);
+#pragma unroll
+        for (int i = 0; i < MI; i++) {
+#pragma unroll
+            for (int j = 0; j < NI; j++) acc[i][j] = mfma<k>(y[j], x[i], acc[i][j], sb[g & 1][j], sa[g & 1][i]);
+            settle();
+            if constexpr (k < 2) load_codes(stage ^ 1, k * 4 + i);
+            settle();
+        }
+        __builtin_amdgcn_s_setprio(0);
+        meet();
+    };
+    const auto whole = [&](auto tile) {
+        turn(std::integral_constant<int, 0>{}, tile);
+        turn(std::integral_constant<int, 1>{}, tile);
+        turn(std::integral_constant<int, 2>{}, tile);
+        turn(std::integral_constant<int, 3>{}, tile);
+        if constexpr (decltype(tile)::value % 2 == 1) take_scales();
+    };
+
+    aim();
+    aim_scales(fq, 0, true);
+#pragma unroll
+    for (int i = 0; i < 8; i++) load_codes(0, i);
+#pragma unroll
+    for (int i = 0; i < G / 2; i++) load_scales(0, i);
+    advance();
+    wait_vmem_below<0>();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 6; i++) read_scales(0, 0, i);
+    take_scales();
+    if (wave >= 4) meet();
+    for (uint32_t t = 0; t < total; t += G) {
+        whole(std::integral_constant<int, 0>{});
+        whole(std::integral_constant<int, 1>{});
+        if constexpr (G == 4) {
+            whole(std::integral_constant<int, 2>{});
+            whole(std::integral_constant<int, 3>{});
+        }
+        buf ^= 1;
+    }
+    if (wave < 4) meet();
+    wait_vmem_below<0>();
+    __syncthreads();
+    static_assert(WAVES * 32 * NI * 32 * T::ESZ <= sizeof(lds.codes), "the results' way out fits the stages");
+    store_results<T, MI, NI>(a, acc, lds.codes[0] + wave * 32 * NI * 32 * T::ESZ, lane, m0 + wm, n0 + wn, SUM ? 0 : q0,
+                             SUM ? a.ranks : q0 + 1);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows of one operand, A here: a stream of the other.  A workgroup has W (32
+// or 16) columns of C (rows of B) and MI x W of its rows; its waves take the
+// contraction's tiles in turn, straight from memory into registers, the next
+// tile's loads in flight while one is multiplied, and the waves' sums meet in LDS,
+// added in wave order.
+// ---------------------------------------------------------------------------
+template <int W>
+struct Wide;
+template <>
+struct Wide<32> {
+    typedef f32x16 Acc;
+    static constexpr int STEPS = 4;
+    // A lane's scales of a tile's steps, from its row's eight bytes.
+    __device__ static void scales(u32x2 bytes, uint32_t part, uint32_t* s)
+    {
+        s[0] = s[1] = s[2] = s[3] = step_scales(bytes, part);
+    }
+    template <int S>
+    __device__ static Acc mul(u32x4 b, u32x4 a, Acc acc, uint32_t sb, uint32_t sa) { return mfma<S>(b, a, acc, sb, sa); }
+    // The column of result e.
+    __device__ static uint32_t col(int e, uint32_t part) { return 8 * (e / 4) + 4 * part + e % 4; }
+};
+template <>
+struct Wide<16> {
+    typedef f32x4 Acc;
+    static constexpr int STEPS = 2;
+    __device__ static void scales(u32x2 bytes, uint32_t part, uint32_t* s)
+    {
+        s[0] = bytes.x >> (8 * part);
+        s[1] = bytes.y >> (8 * part);
+    }
+    template <int S>
+    __device__ static Acc mul(u32x4 b, u32x4 a, Acc acc, uint32_t sb, uint32_t sa)
+    {
+        const i32x8 x = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+        const i32x8 y = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 4, 4, 0, (int)sb, 0, (int)sa);
+    }
+    __device__ static uint32_t col(int e, uint32_t part) { return 4 * part + e; }
+};
+
+template <int W, int MI>
 struct Frag {
-    u32x4 b[4], a[MI][4];
+    u32x4 b[Wide<W>::STEPS], a[MI][Wide<W>::STEPS];
     u32x2 sb, sa[MI];
 };
 
-template <class T, bool SUM, int MI, int WAVES>
+template <class T, bool SUM, int W, int MI, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void k_mx4_matmul_few(MatmulArgs a)
 {
-    __shared__ float part[WAVES][MI * 32 * 33];
+    typedef Wide<W> Op;
+    constexpr int STEPS = Op::STEPS, PARTS = 64 / W, RESULTS = W * W / 64;
+    __shared__ float part_sum[WAVES][MI * W * (W + 1)];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t r = lane & 31, half = lane >> 5;
-    const uint32_t n0 = blockIdx.x * 32;
+    const uint32_t r = lane % W, part = lane / W;
+    const uint32_t n0 = blockIdx.x % a.tiles_n * W, m0 = blockIdx.x / a.tiles_n * (MI * W);
     const uint32_t ktiles = (a.kb + kTileBlocks - 1) / kTileBlocks;
     const int q0 = SUM ? 0 : (int)blockIdx.y;
     const uint32_t total = ktiles * (SUM ? (uint32_t)a.ranks : 1u);
     const uint64_t rb = n0 + r < a.n ? n0 + r : a.n - 1;
     uint64_t ra[MI];
 #pragma unroll
-    for (int i = 0; i < MI; i++) ra[i] = i * 32 + r < a.m ? i * 32 + r : a.m - 1;
+    for (int i = 0; i < MI; i++) ra[i] = m0 + i * W + r < a.m ? m0 + i * W + r : a.m - 1;
 
-    const auto fetch = [&](Frag<MI>& f, uint32_t t) {
+    const auto fetch = [&](Frag<W, MI>& f, uint32_t t) {
         const uint32_t qi = t / ktiles, kt = t - qi * ktiles;
         const int q = q0 + (int)qi;
         const uint64_t k0 = (uint64_t)kt * kTileBlocks;
         const uint32_t left = a.kb - kt * kTileBlocks;
-        const char* pb = a.bc[q] + (rb * a.kb + k0 + half) * 16;
-        f.sb = load_scales(a.bs[q] + rb * a.kb + k0, left);
+        f.sb = row_of_scales(a.bs[q] + rb * a.kb + k0, left);
 #pragma unroll
-        for (int i = 0; i < MI; i++) f.sa[i] = load_scales(a.as[q] + ra[i] * a.kb + k0, left);
+        for (int i = 0; i < MI; i++) f.sa[i] = row_of_scales(a.as[q] + ra[i] * a.kb + k0, left);
+        const char* pb = a.bc[q] + (rb * a.kb + k0 + part) * 16;
         if (left >= kTileBlocks) {
 #pragma unroll
-            for (int s = 0; s < 4; s++) f.b[s] = *(global_ptr<const u32x4>)(pb + 32 * s);
+            for (int s = 0; s < STEPS; s++) f.b[s] = *(global_ptr<const u32x4>)(pb + PARTS * 16 * s);
 #pragma unroll
             for (int i = 0; i < MI; i++) {
-                const char* pa = a.ac[q] + (ra[i] * a.kb + k0 + half) * 16;
+                const char* pa = a.ac[q] + (ra[i] * a.kb + k0 + part) * 16;
 #pragma unroll
-                for (int s = 0; s < 4; s++) f.a[i][s] = *(global_ptr<const u32x4>)(pa + 32 * s);
+                for (int s = 0; s < STEPS; s++) f.a[i][s] = *(global_ptr<const u32x4>)(pa + PARTS * 16 * s);
             }
         } else {
 #pragma unroll
-            for (int s = 0; s < 4; s++) f.b[s] = 2 * s + half < left ? *(global_ptr<const u32x4>)(pb + 32 * s) : u32x4{};
+            for (int s = 0; s < STEPS; s++)
+                f.b[s] = PARTS * s + part < left ? *(global_ptr<const u32x4>)(pb + PARTS * 16 * s) : u32x4{};
 #pragma unroll
             for (int i = 0; i < MI; i++) {
-                const char* pa = a.ac[q] + (ra[i] * a.kb + k0 + half) * 16;
+                const char* pa = a.ac[q] + (ra[i] * a.kb + k0 + part) * 16;
 #pragma unroll
-                for (int s = 0; s < 4; s++)
-                    f.a[i][s] = 2 * s + half < left ? *(global_ptr<const u32x4>)(pa + 32 * s) : u32x4{};
+                for (int s = 0; s < STEPS; s++)
+                    f.a[i][s] = PARTS * s + part < left ? *(global_ptr<const u32x4>)(pa + PARTS * 16 * s) : u32x4{};
             }
         }
     };
-    f32x16 acc[MI] = {};
-    const auto multiply = [&](const Frag<MI>& f) {
-        const uint32_t sb = step_scales(f.sb, half);
+    typename Op::Acc acc[MI] = {};
+    const auto multiply = [&](const Frag<W, MI>& f) {
+        uint32_t sb[STEPS];
+        Op::scales(f.sb, part, sb);
 #pragma unroll
         for (int i = 0; i < MI; i++) {
-            const uint32_t sa = step_scales(f.sa[i], half);
-            acc[i] = mfma<0>(f.b[0], f.a[i][0], acc[i], sb, sa);
-            acc[i] = mfma<1>(f.b[1], f.a[i][1], acc[i], sb, sa);
-            acc[i] = mfma<2>(f.b[2], f.a[i][2], acc[i], sb, sa);
-            acc[i] = mfma<3>(f.b[3], f.a[i][3], acc[i], sb, sa);
+            uint32_t sa[STEPS];
+            Op::scales(f.sa[i], part, sa);
+            acc[i] = Op::template mul<0>(f.b[0], f.a[i][0], acc[i], sb[0], sa[0]);
+            acc[i] = Op::template mul<1>(f.b[1], f.a[i][1], acc[i], sb[1], sa[1]);
+            if constexpr (STEPS == 4) {
+                acc[i] = Op::template mul<2>(f.b[2], f.a[i][2], acc[i], sb[2], sa[2]);
+                acc[i] = Op::template mul<3>(f.b[3], f.a[i][3], acc[i], sb[3], sa[3]);
+            }
         }
     };
-    Frag<MI> f0, f1;
+    Frag<W, MI> f0, f1;
     uint32_t t = wave;
     if (t < total) fetch(f0, t);
     for (; t < total; t += 2 * WAVES) {
@@ -353,24 +743,24 @@ __global__ __launch_bounds__(WAVES * 64) void k_mx4_matmul_few(MatmulArgs a)
 #pragma unroll
     for (int i = 0; i < MI; i++)
 #pragma unroll
-        for (int e = 0; e < 16; e++) part[wave][(i * 32 + r) * 33 + 8 * (e / 4) + 4 * half + e % 4] = acc[i][e];
+        for (int e = 0; e < RESULTS; e++) part_sum[wave][(i * W + r) * (W + 1) + Op::col(e, part)] = acc[i][e];
     __syncthreads();
     const int dst0 = SUM ? 0 : q0, dst1 = SUM ? a.ranks : q0 + 1;
-    for (uint32_t o = tid; o < MI * 32 * 32; o += WAVES * 64) {
-        const uint32_t row = o / 32, col = o % 32;
-        if (row >= a.m || n0 + col >= a.n) continue;
-        float s = part[0][row * 33 + col];
+    for (uint32_t o = tid; o < MI * W * W; o += WAVES * 64) {
+        const uint32_t row = o / W, col = o % W;
+        if (m0 + row >= a.m || n0 + col >= a.n) continue;
+        float s = part_sum[0][row * (W + 1) + col];
 #pragma unroll
-        for (int w = 1; w < WAVES; w++) s += part[w][row * 33 + col];
+        for (int w = 1; w < WAVES; w++) s += part_sum[w][row * (W + 1) + col];
         const typename T::S v = T::narrow(s);
-        const uint64_t at = ((uint64_t)row * a.n + n0 + col) * T::ESZ;
+        const uint64_t at = ((m0 + row) * a.sm + (n0 + col) * a.sn) * T::ESZ;
         for (int d = dst0; d < dst1; d++) store_s<T>(a.dst[d] + at, v);
     }
 }
 
 using namespace host;
 
-template <class T, bool SUM, int BM, int BN, int WM, int WN>
+template <class T, bool SUM, bool EVEN, int BM, int BN, int WM, int WN, int S>
 vrc_status_t launch_tiled(MatmulArgs& a, hipStream_t st)
 {
     a.tiles_m = (a.m + BM - 1) / BM;
@@ -378,27 +768,79 @@ vrc_status_t launch_tiled(MatmulArgs& a, hipStream_t st)
     const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
     if (tiles > 0x7fffffffull) return VRC_ERR_INVALID_ARG;
     const dim3 grid((unsigned)tiles, SUM ? 1u : (unsigned)a.ranks);
-    k_mx4_matmul_tiled<T, SUM, BM, BN, WM, WN><<<grid, WM * WN * 64, 0, st>>>(a);
+    k_mx4_matmul_tiled<T, SUM, EVEN, BM, BN, WM, WN, S><<<grid, WM * WN * 64, 0, st>>>(a);
     return check_launch();
 }
 
-template <class T, bool SUM, int MI>
-vrc_status_t launch_few(const MatmulArgs& a, hipStream_t st)
+template <class T, bool SUM, int G>
+vrc_status_t launch_turns(MatmulArgs& a, hipStream_t st)
 {
-    constexpr int WAVES = 8;
-    const dim3 grid((a.n + 31) / 32, SUM ? 1u : (unsigned)a.ranks);
-    k_mx4_matmul_few<T, SUM, MI, WAVES><<<grid, WAVES * 64, 0, st>>>(a);
+    a.tiles_m = (a.m + 255) / 256;
+    a.tiles_n = (a.n + 255) / 256;
+    const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
+    if (tiles > 0x7fffffffull) return VRC_ERR_INVALID_ARG;
+    k_mx4_matmul_turns<T, SUM, G><<<dim3((unsigned)tiles, SUM ? 1u : (unsigned)a.ranks), 512, 0, st>>>(a);
     return check_launch();
 }
 
+// `swap`: B is the operand of few rows.
+template <class T, bool SUM, int W, int MI, int WAVES>
+vrc_status_t launch_few(MatmulArgs a, bool swap, hipStream_t st)
+{
+    a.sm = a.n;
+    a.sn = 1;
+    if (swap) {
+        for (int r = 0; r < a.ranks; r++) {
+            std::swap(a.ac[r], a.bc[r]);
+            std::swap(a.as[r], a.bs[r]);
+        }
+        std::swap(a.m, a.n);
+        std::swap(a.sm, a.sn);
+    }
+    a.tiles_m = (a.m + MI * W - 1) / (MI * W);
+    a.tiles_n = (a.n + W - 1) / W;
+    const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
+    if (tiles > 0x7fffffffull) return VRC_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)tiles, SUM ? 1u : (unsigned)a.ranks);
+    k_mx4_matmul_few<T, SUM, W, MI, WAVES><<<grid, WAVES * 64, 0, st>>>(a);
+    return check_launch();
+}
+
+// The kernel by sizes.  One operand of up to 64 rows: a stream of the other, by 16
+// columns where that makes at most a workgroup per CU and by 32 otherwise (us; 16 /
+// 32 columns: 1 x 4096 x 16384 9.5 / 14.0, 32 x 4096 x 16384 18.5 / 20.6; but
+// 1 x 8192 x 8 x 4096 29.6 / 26.5, 32 x 8192 x 4096 10.4 / 7.5, and from 33 rows
+// 48 x 5003 x 4 x 1000 14.5 / 9.6).  Else the smallest tiles of which at most two a CU
+// are needed: a tile of the contraction takes 0.5 us with 64 x 64 tiles, 0.7 us with
+// 128 x 128 and 1.2 us with 256 x 256, whatever the grid, until the CUs are full
+// (us; 64 / 128 / 256: 256 x 8192 x 4096 12.5 / 15.0 / 24.0, 512 x 8192 x 4096
+// 23.4 / 16.7 / 25.3, 1024 x 8192 x 4096 45.7 / 25.6 / 28.1, 2048 x 8192 x 4096
+// 84.5 / 48.9 / 38.7).
 template <class T, bool SUM>
 vrc_status_t matmul_typed(MatmulArgs& a, int cus, hipStream_t st)
 {
-    if (a.m <= 32) return launch_few<T, SUM, 1>(a, st);
-    if (a.m <= 64) return launch_few<T, SUM, 2>(a, st);
-    const uint64_t big = (uint64_t)((a.m + 255) / 256) * ((a.n + 255) / 256) * (SUM ? 1 : a.ranks);
-    if (big >= (uint64_t)cus) return launch_tiled<T, SUM, 256, 256, 2, 4>(a, st);
-    return launch_tiled<T, SUM, 128, 128, 2, 2>(a, st);
+    const bool swap = a.n < a.m;
+    const uint32_t few = swap ? a.n : a.m, many = swap ? a.m : a.n;
+    const uint64_t products = SUM ? 1 : (uint64_t)a.ranks;
+    // A lane of the ragged tiles reads eight scale bytes at once, so an array has eight.
+    const bool tiny = (uint64_t)few * a.kb < 8;
+    if (few <= 64 || tiny) {
+        if (few > 32 && !tiny) return launch_few<T, SUM, 32, 2, 8>(a, swap, st);
+        const bool by16 = ((many + 15ull) / 16) * products <= (uint64_t)cus;
+        if (few <= 16 || tiny) return by16 ? launch_few<T, SUM, 16, 1, 8>(a, swap, st) : launch_few<T, SUM, 32, 1, 8>(a, swap, st);
+        return by16 ? launch_few<T, SUM, 16, 2, 8>(a, swap, st) : launch_few<T, SUM, 32, 1, 8>(a, swap, st);
+    }
+    bool even = a.kb % (2 * kTileBlocks) == 0;
+    for (int r = 0; r < a.ranks; r++) even = even && (uintptr_t)a.as[r] % 16 == 0 && (uintptr_t)a.bs[r] % 16 == 0;
+    const auto tiles = [&](uint64_t b) { return ((a.m + b - 1) / b) * ((a.n + b - 1) / b) * products; };
+    const uint64_t room = 2 * (uint64_t)cus;
+    if (!even) {
+        if (tiles(64) <= room) return launch_tiled<T, SUM, false, 64, 64, 1, 2, 2>(a, st);
+        return launch_tiled<T, SUM, false, 128, 128, 2, 2, 2>(a, st);
+    }
+    if (tiles(64) <= room) return launch_tiled<T, SUM, true, 64, 64, 1, 2, 4>(a, st);
+    if (tiles(128) <= room) return launch_tiled<T, SUM, true, 128, 128, 2, 2, 2>(a, st);
+    return a.kb % (4 * kTileBlocks) == 0 ? launch_turns<T, SUM, 4>(a, st) : launch_turns<T, SUM, 2>(a, st);
 }
 
 }  // namespace

@@ -11,8 +11,8 @@ import contextlib
 import ctypes as C
 import os
 
-from . import (PKG, VRC_BF16, VRC_FP16, VRC_FP32, VRC_OK, VrcError, _check_ranks, _dtype_code, _outer, _prod,
-               _ptr_array, _stream, _torch, chunk_range, reduce_scatter_shape)
+from . import (MAX_RANKS, PKG, VRC_BF16, VRC_FP16, VRC_FP32, VRC_OK, VrcError, _check_ranks, _dtype_code, _outer,
+               _prod, _stream, _torch, chunk_range, reduce_scatter_shape)
 
 OPS_LIB_PATH = os.path.join(PKG, "libvrc_ops.so")
 OPS_VERSION = 100  # VRC_OPS_VERSION of include/vrc_ops.h that this binding follows
@@ -66,8 +66,11 @@ def _done(status: int, where: str):
         raise VrcError(status, where, _ops.vrc_ops_last_hip_error())
 
 
+_POINTERS = [C.c_void_p * n for n in range(MAX_RANKS + 1)]
+
+
 def _pointers(tensors):
-    return _ptr_array([t.data_ptr() for t in tensors])
+    return _POINTERS[len(tensors)](*[t.data_ptr() for t in tensors])
 
 
 @contextlib.contextmanager
@@ -81,20 +84,34 @@ def _allocating(stream):
             yield
 
 
+# New outputs of one shape are views of one allocation while each holds at most
+# this many bytes, and a multiple of 128 (so that all sit on one grid): eight
+# allocations cost 14 us of host time, one with its views 5 us, which is
+# what a small call takes; larger calls hide it, and keep tensors that can be freed
+# one by one.
+SHARED_ALLOCATION_BYTES = 4 << 20
+
+
 def _outputs(recv, shapes, like, where, stream, dtype=None):
     """`recv` checked against one shape per rank, or new tensors."""
     torch = _torch()
     dtype = like.dtype if dtype is None else dtype
+    n, device = len(shapes), like.device
     if recv is None:
+        first = shapes[0]
         with _allocating(stream):
-            return [torch.empty(s, dtype=dtype, device=like.device) for s in shapes]
-    if not isinstance(recv, (list, tuple)) or len(recv) != len(shapes):
+            size = _prod(first) * dtype.itemsize
+            if n > 1 and size <= SHARED_ALLOCATION_BYTES and size % 128 == 0 and all(s == first for s in shapes):
+                return list(torch.empty((n, *first), dtype=dtype, device=device).unbind(0))
+            return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
+    if not isinstance(recv, (list, tuple)) or len(recv) != n:
         raise ValueError(f"{where}: one output per rank")
+    at = like.get_device()
     for c, (t, s) in enumerate(zip(recv, shapes)):
-        if t.numel() != _prod(s) or t.dtype != dtype or not t.is_contiguous():
+        if t.dtype is not dtype or t.numel() != _prod(s) or not t.is_contiguous():
             raise ValueError(f"{where}: output {c} must be contiguous {tuple(s)} {dtype}")
-        if t.device != like.device:
-            raise ValueError(f"{where}: outputs must be on the inputs' device {like.device}")
+        if t.get_device() != at:
+            raise ValueError(f"{where}: outputs must be on the inputs' device {device}")
     return recv
 
 
@@ -143,17 +160,20 @@ def vrc_allreduce_dropout(send, p, seed, offset=0, residual=None, recv=None, str
     torch = _torch()
     dev = _check_ranks(send, where)
     code = _float_code(send[0], where)
-    shapes = [tuple(send[0].shape)] * len(send)
+    n = len(send)
+    shape = tuple(send[0].shape)
+    shapes = [shape] * n
+    res = None
     if isinstance(residual, torch.Tensor):
-        residual = [residual] * len(send)
-    if residual is not None:
-        _residuals(residual, shapes, send[0], where)
+        _residuals([residual], [shape], send[0], where)
+        res = _POINTERS[n](*[residual.data_ptr()] * n)
+    elif residual is not None:
+        res = _pointers(_residuals(residual, shapes, send[0], where))
     drop = _dropout(p, seed, offset, send[0].device, where)
     st = _stream(stream, dev)
     recv = _outputs(recv, shapes, send[0], where, stream)
-    _done(_ops.vrc_allreduce_dropout(_pointers(send), None if residual is None else _pointers(residual),
-                                     _pointers(recv), len(send), send[0].numel(), code, C.byref(drop), st or None),
-          where)
+    _done(_ops.vrc_allreduce_dropout(_pointers(send), res, _pointers(recv), n, send[0].numel(), code, C.byref(drop),
+                                     st or None), where)
     return recv
 
 
@@ -261,11 +281,10 @@ def _quantised(codes, scales, where):
     """(leading shape, blocks per row, device index) of one matrix per rank."""
     torch = _torch()
     dev = _check_ranks(codes, where)
-    _check_ranks(scales, where)
-    if codes[0].dtype != torch.uint8 or scales[0].dtype != torch.uint8:
-        raise TypeError(f"{where}: codes and scales are uint8")
-    if len(scales) != len(codes) or scales[0].device != codes[0].device:
+    if _check_ranks(scales, where) != dev or len(scales) != len(codes):
         raise ValueError(f"{where}: one scales tensor per codes tensor, on its device")
+    if codes[0].dtype is not torch.uint8 or scales[0].dtype is not torch.uint8:
+        raise TypeError(f"{where}: codes and scales are uint8")
     lead, kb = tuple(scales[0].shape[:-1]), scales[0].shape[-1] if scales[0].dim() else 0
     if scales[0].dim() == 0 or tuple(codes[0].shape) != lead + (kb * 16,):
         raise ValueError(f"{where}: codes must be [..., 16 KB] beside scales [..., KB]")

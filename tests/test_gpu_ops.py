@@ -427,7 +427,9 @@ def check_product(got, y, mag, k, dtype, what):
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("m,nc,k", [(1, 1, 1), (1, 16, 32), (2, 40, 64), (3, 100, 2048), (16, 16, 96), (17, 33, 200), (31, 257, 500),
-                                    (64, 64, 128), (65, 63, 1000), (100, 300, 333), (128, 130, 4100), (257, 255, 160), (300, 520, 1024)])
+                                    (64, 64, 128), (65, 63, 1000), (100, 300, 333), (128, 130, 4100), (257, 255, 160), (300, 520, 1024),
+                                    (500, 1, 2048), (1000, 20, 96), (300, 64, 70), (200, 3, 64), (3, 200, 64), (400, 1, 20), (80, 1100, 1536),
+                                    (3000, 2, 300), (20, 700, 512), (700, 24, 90), (1, 9000, 96), (30, 9000, 96), (2, 3, 40)])
 def test_mx4_matmul(vrc, dtype, m, nc, k):
     for n in (1, 3):
         say(f"mx4_matmul {dtype} n={n} m={m} n={nc} k={k}")
@@ -457,7 +459,9 @@ def test_mx4_matmul_many_ranks(vrc, n):
             assert (out[r] == 3.0).all(), "written outside"
 
 
-@pytest.mark.parametrize("join,n,m,nc,k", [("sum", 1, 4001, 4100, 200), ("sum", 2, 4096, 4096, 96), ("each", 4, 2050, 1999, 300)])
+@pytest.mark.parametrize("join,n,m,nc,k", [("sum", 1, 4001, 4100, 200), ("sum", 2, 4096, 4096, 96), ("each", 4, 2050, 1999, 300),
+                                           ("sum", 3, 4001, 4100, 512), ("sum", 1, 4090, 3900, 2560), ("sum", 2, 4096, 4096, 1024),
+                                           ("each", 4, 2050, 1999, 2048), ("each", 5, 2000, 2048, 1536)])
 def test_mx4_matmul_large_tiles(vrc, join, n, m, nc, k):
     """Enough work for the largest tiles, ragged and whole."""
     a, b = [random_mx4(m, k, r) for r in range(n)], [random_mx4(nc, k, 90 + r) for r in range(n)]

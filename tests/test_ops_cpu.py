@@ -43,7 +43,7 @@ def test_header_compiles_as_c(tmp_path):
 
 
 def arr(base, n, stride=1 << 20):
-    return ops._ptr_array([base + r * stride for r in range(n)])
+    return vrc._ptr_array([base + r * stride for r in range(n)])
 
 
 def drop(p=0.5, seed=1, offset=2, dev=None):
@@ -58,8 +58,8 @@ def test_dropout_refusals():
         return L.vrc_allreduce_dropout(x, res, y, n, count, dt, d, None)
 
     assert ar(n=0) == ar(n=17) == ar(count=(1 << 56) + 1) == vrc.VRC_ERR_INVALID_ARG
-    assert ar(x=None) == ar(y=None) == ar(x=ops._ptr_array([A, None, A, A])) == vrc.VRC_ERR_INVALID_ARG
-    assert ar(res=ops._ptr_array([R, R, None, R])) == vrc.VRC_ERR_INVALID_ARG
+    assert ar(x=None) == ar(y=None) == ar(x=vrc._ptr_array([A, None, A, A])) == vrc.VRC_ERR_INVALID_ARG
+    assert ar(res=vrc._ptr_array([R, R, None, R])) == vrc.VRC_ERR_INVALID_ARG
     assert ar(dt=vrc.VRC_INT32) == ar(dt=9) == ar(dt=-1) == vrc.VRC_ERR_UNSUPPORTED
     for p in (-0.1, 1.0001, float("nan"), float("inf")):
         assert ar(d=drop(p)) == vrc.VRC_ERR_INVALID_ARG
@@ -67,17 +67,17 @@ def test_dropout_refusals():
     assert ar(count=0, x=None, y=None) == vrc.VRC_OK
     # overlaps: an output inside an input, in a residual, in another output; send[q] as recv[r]
     assert ar(y=arr(A + 2, 4)) == vrc.VRC_ERR_ALIAS
-    assert ar(y=ops._ptr_array([A + (1 << 20), A, B, B + 4096])) == vrc.VRC_ERR_ALIAS
-    assert ar(y=ops._ptr_array([B, B, R, R + 4096])) == vrc.VRC_ERR_ALIAS
+    assert ar(y=vrc._ptr_array([A + (1 << 20), A, B, B + 4096])) == vrc.VRC_ERR_ALIAS
+    assert ar(y=vrc._ptr_array([B, B, R, R + 4096])) == vrc.VRC_ERR_ALIAS
     assert ar(res=arr(R, 4), y=arr(R + 1998, 4)) == vrc.VRC_ERR_ALIAS
-    shared = ops._ptr_array([R] * 4)
-    assert ar(res=shared, y=ops._ptr_array([R, B, B + 4096, B + 8192])) == vrc.VRC_ERR_ALIAS
+    shared = vrc._ptr_array([R] * 4)
+    assert ar(res=shared, y=vrc._ptr_array([R, B, B + 4096, B + 8192])) == vrc.VRC_ERR_ALIAS
 
     def rs(x=arr(A, 4), res=None, y=arr(B, 4), n=4, count=1000, outer=1, dt=vrc.VRC_BF16, d=drop()):
         return L.vrc_reduce_scatter_dropout(x, res, y, n, count, outer, dt, d, None)
 
     assert rs(outer=0) == rs(outer=3) == rs(count=1000, outer=500) == vrc.VRC_ERR_INVALID_ARG
-    assert rs(y=arr(A, 4)) == rs(res=arr(R, 4), y=ops._ptr_array([R + (1 << 20), B, B + 4096, B + 8192])) == vrc.VRC_ERR_ALIAS
+    assert rs(y=arr(A, 4)) == rs(res=arr(R, 4), y=vrc._ptr_array([R + (1 << 20), B, B + 4096, B + 8192])) == vrc.VRC_ERR_ALIAS
     assert rs(d=drop(2.0)) == vrc.VRC_ERR_INVALID_ARG
     assert rs(dt=vrc.VRC_INT32) == vrc.VRC_ERR_UNSUPPORTED
     assert rs(count=0) == vrc.VRC_OK
@@ -86,7 +86,7 @@ def test_dropout_refusals():
         return L.vrc_all_gather_dropout(x, y, n, total, outer, dt, d, None)
 
     assert ag(outer=0) == ag(outer=500) == ag(x=None) == ag(y=arr(0, 4)) == vrc.VRC_ERR_INVALID_ARG
-    assert ag(y=arr(A + 100, 4)) == ag(y=ops._ptr_array([B, B + 1998, R, R + 4096])) == vrc.VRC_ERR_ALIAS
+    assert ag(y=arr(A + 100, 4)) == ag(y=vrc._ptr_array([B, B + 1998, R, R + 4096])) == vrc.VRC_ERR_ALIAS
     assert ag(dt=vrc.VRC_INT32) == vrc.VRC_ERR_UNSUPPORTED
 
 
@@ -118,7 +118,7 @@ def test_mx4_refusals():
     assert mm(y=None) == mm(ac=arr(A + 4, 2)) == mm(bc=arr(B + 8, 2)) == vrc.VRC_ERR_INVALID_ARG
     assert mm(m=1 << 31) == mm(nc=1 << 31) == mm(kb=1 << 20) == mm(m=1 << 30, nc=1 << 30) == vrc.VRC_ERR_INVALID_ARG
     assert mm(dt=vrc.VRC_INT32) == mm(join=2) == vrc.VRC_ERR_UNSUPPORTED
-    assert mm(y=arr(A, 2)) == mm(y=arr(B + (1 << 28), 2)) == mm(y=ops._ptr_array([R, R + 64])) == vrc.VRC_ERR_ALIAS
+    assert mm(y=arr(A, 2)) == mm(y=arr(B + (1 << 28), 2)) == mm(y=vrc._ptr_array([R, R + 64])) == vrc.VRC_ERR_ALIAS
     assert mm(m=0) == mm(nc=0) == vrc.VRC_OK
 
 
