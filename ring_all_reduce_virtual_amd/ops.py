@@ -7,7 +7,6 @@ kernels.  Where a ``stream`` is given, outputs that the call allocates belong
 to that stream's pool."""
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 
@@ -73,37 +72,36 @@ def _pointers(tensors):
     return _POINTERS[len(tensors)](*[t.data_ptr() for t in tensors])
 
 
-@contextlib.contextmanager
-def _allocating(stream):
-    """Allocations inside belong to `stream` (the current one if None): a block
-    of another stream's pool might still be in use there."""
-    if stream is None:
-        yield
-    else:
-        with _torch().cuda.stream(stream):
-            yield
-
-
 # New outputs of one shape are views of one allocation while each holds at most
-# this many bytes, and a multiple of 128 (so that all sit on one grid): eight
-# allocations cost 14 us of host time, one with its views 5 us, which is
-# what a small call takes; larger calls hide it, and keep tensors that can be freed
-# one by one.
+# this many bytes, in whole vectors: eight allocations cost 14 us of host time, one
+# with its views 5 us, which is what a small call takes; larger calls hide it, and
+# keep tensors that can be freed one by one.
 SHARED_ALLOCATION_BYTES = 4 << 20
 
 
-def _outputs(recv, shapes, like, where, stream, dtype=None):
-    """`recv` checked against one shape per rank, or new tensors."""
+def _allocate(shapes, dtype, device):
     torch = _torch()
+    first, n = shapes[0], len(shapes)
+    if n > 1 and shapes.count(first) == n:
+        size = _prod(first) * dtype.itemsize
+        if size <= SHARED_ALLOCATION_BYTES and size % 16 == 0:
+            return list(torch.empty((n, *first), dtype=dtype, device=device).unbind(0))
+        t0 = torch.empty(first, dtype=dtype, device=device)
+        return [t0] + [torch.empty_like(t0) for _ in range(n - 1)]
+    return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
+
+
+def _outputs(recv, shapes, like, where, stream, dtype=None):
+    """`recv` checked against one shape per rank, or new tensors.  Those belong to
+    `stream` if one is given: a block of another stream's pool might still be in use
+    there."""
     dtype = like.dtype if dtype is None else dtype
     n, device = len(shapes), like.device
     if recv is None:
-        first = shapes[0]
-        with _allocating(stream):
-            size = _prod(first) * dtype.itemsize
-            if n > 1 and size <= SHARED_ALLOCATION_BYTES and size % 128 == 0 and all(s == first for s in shapes):
-                return list(torch.empty((n, *first), dtype=dtype, device=device).unbind(0))
-            return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
+        if stream is None:
+            return _allocate(shapes, dtype, device)
+        with _torch().cuda.stream(stream):
+            return _allocate(shapes, dtype, device)
     if not isinstance(recv, (list, tuple)) or len(recv) != n:
         raise ValueError(f"{where}: one output per rank")
     at = like.get_device()
