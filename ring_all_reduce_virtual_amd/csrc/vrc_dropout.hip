@@ -16,6 +16,12 @@ namespace {
 
 using host::MaskArgs;
 
+// a ^ b ^ c in one instruction (the compiler makes two).
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c)
+{
+    return (uint32_t)__builtin_amdgcn_bitop3_b32((int)a, (int)b, (int)c, 0x96);
+}
+
 // One Philox-4x32 bijection of ten rounds: counter (block, offset), key seed.
 __device__ __forceinline__ void philox(uint64_t block, uint64_t offset, uint64_t seed, uint32_t w[4])
 {
@@ -25,8 +31,8 @@ __device__ __forceinline__ void philox(uint64_t block, uint64_t offset, uint64_t
 #pragma unroll
     for (int r = 0; r < 10; r++) {
         const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
-        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+        c0 = xor3((uint32_t)(p1 >> 32), c1, k0);
+        c2 = xor3((uint32_t)(p0 >> 32), c3, k1);
         c1 = (uint32_t)p1;
         c3 = (uint32_t)p0;
         k0 += 0x9E3779B9u;
@@ -107,10 +113,11 @@ __device__ __forceinline__ u32x4 add_residual(const float* acc, u32x4 res)
 }
 
 // ---------------------------------------------------------------------------
-// All-reduce.  One-wave workgroups; a wave takes U consecutive 1 KiB tiles of
-// every buffer an iteration with all its loads in flight.  A lane reads its
-// elements of every input and residual before it writes any output, so an
-// output may be its own input or residual.
+// All-reduce.  One-wave workgroups, a 1 KiB tile of every buffer an iteration
+// with all its loads in flight (2, 4 or 8 tiles at once, with fewer waves, came to
+// within 3 % of the best either way).  A lane reads its elements of every input and
+// residual before it writes any output, so an output may be its own input or
+// residual.
 // RES: 0 none, 1 one residual for all ranks, 2 one for each.
 // ---------------------------------------------------------------------------
 struct DropArArgs {
@@ -121,45 +128,33 @@ struct DropArArgs {
     MaskArgs m;
 };
 
-template <class T, int N, int RES, int U>
+template <class T, int N, int RES>
 __global__ __launch_bounds__(64) void k_dropout_allreduce(DropArArgs a)
 {
     constexpr uint64_t W = 64, E = T::ESZ;
     constexpr int NR = RES == 2 ? N : RES;
     const Mask mask(a.m);
     const uint64_t body = a.g.head * E, nv = a.g.nvb, lane = threadIdx.x;
-    const auto tile = [&](uint64_t v, int groups) {
-        u32x4 in[U][N], res[U][NR ? NR : 1];
+    for (uint64_t v = blockIdx.x * W + lane; v < nv; v += (uint64_t)gridDim.x * W) {
+        u32x4 in[N], res[NR ? NR : 1];
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            if (u >= groups) break;
+        for (int r = 0; r < N; r++) in[r] = ld16<true>(a.src[r] + body + v * 16);
 #pragma unroll
-            for (int r = 0; r < N; r++) in[u][r] = ld16<true>(a.src[r] + body + (v + u * W) * 16);
-#pragma unroll
-            for (int r = 0; r < NR; r++) res[u][r] = ld16<true>(a.res[r] + body + (v + u * W) * 16);
-        }
+        for (int r = 0; r < NR; r++) res[r] = ld16<true>(a.res[r] + body + v * 16);
         issue_loads_first();
+        float acc[T::VEC];
+        fold_f32<T, N>(in, acc);
+        const uint32_t bits = mask.keep<T::VEC>(a.g.head + v * T::VEC);
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            if (u >= groups) break;
-            const uint64_t at = v + u * W;
-            float acc[T::VEC];
-            fold_f32<T, N>(in[u], acc);
-            const uint32_t bits = mask.keep<T::VEC>(a.g.head + at * T::VEC);
+        for (int i = 0; i < T::VEC; i++) acc[i] = mask.apply(acc[i], bits, i);
+        u32x4 out = RES == 0 ? T::pack(acc) : u32x4{};
+        if constexpr (RES == 1) out = add_residual<T>(acc, res[0]);
 #pragma unroll
-            for (int i = 0; i < T::VEC; i++) acc[i] = mask.apply(acc[i], bits, i);
-            u32x4 out = RES == 0 ? T::pack(acc) : u32x4{};
-            if constexpr (RES == 1) out = add_residual<T>(acc, res[u][0]);
-#pragma unroll
-            for (int r = 0; r < N; r++) {
-                if constexpr (RES == 2) out = add_residual<T>(acc, res[u][r]);
-                st16<true>(a.dst[r] + body + at * 16, out);
-            }
+        for (int r = 0; r < N; r++) {
+            if constexpr (RES == 2) out = add_residual<T>(acc, res[r]);
+            st16<true>(a.dst[r] + body + v * 16, out);
         }
-    };
-    const uint64_t groups = nv / W / U;
-    for (uint64_t g = blockIdx.x; g < groups; g += gridDim.x) tile(g * U * W + lane, U);
-    for (uint64_t v = (groups * U + blockIdx.x) * W + lane; v < nv; v += (uint64_t)gridDim.x * W) tile(v, 1);
+    }
 
     const uint64_t ns = a.g.head + a.g.tail;
     for (uint64_t k = blockIdx.x * W + lane; k < ns; k += (uint64_t)gridDim.x * W) {
@@ -332,11 +327,41 @@ unsigned wave_grid(uint64_t tiles, int cus, int per_cu)
     return (unsigned)(g < 1 ? 1 : g);
 }
 
+// Waves per CU, by the 16-byte loads that a lane has in flight and the bytes that
+// the call moves.  Measured on MI355X, bf16, 2 GB moved (TB/s):
+//   all-reduce, ranks (+ residuals): 1: 16 waves 5.2, 8 waves 4.8; 1 + 1: 8 6.0,
+//   16 5.7; 2: 8 6.0, 16 5.3; 4: 4 6.0, 8 5.8; 8: 4 5.85, 8 5.5; 8 + 1: 4 5.8, 2 5.75;
+//   6 + 6: 2 6.1, 4 5.75; 8 + 8: 2 5.9, 4 5.8, 16 5.4; 16: 2 5.6, 4 5.5;
+//   reduce-scatter: 1: 16 4.8, 8 3.8; 2: 16 5.4, 8 5.2; 2 + 1: 8 5.9, 16 5.6; 4: 8 6.0,
+//   4 4.9; 8: 4 5.6, 8 5.2; 16: 4 5.4, 8 5.2.
+// A call that the 256 MB Infinity Cache holds is better off with more (100 MB,
+// all-reduce of 2: 16 waves 5.6, 4 4.3; of 8 + 8: 16 6.1, 2 5.6).
+constexpr uint64_t kCached = 256ull << 20;
+
+int allreduce_waves(int loads, uint64_t bytes)
+{
+    if (bytes <= kCached) return loads <= 1 ? 32 : 16;
+    return loads <= 1 ? 16 : loads <= 3 ? 8 : loads <= 9 ? 4 : 2;
+}
+
+int reduce_scatter_waves(int loads, uint64_t bytes)
+{
+    if (bytes <= kCached) return loads <= 1 ? 32 : 16;
+    return loads <= 2 ? 16 : loads <= 5 ? 8 : 4;
+}
+
+// The all-gather reads one vector per lane and stores it to every rank: 64 waves per
+// CU (one rank 4.6 TB/s, 16 waves 4.2; 8 ranks 4.8 with 8 to 64, and 1 store in
+// flight per wave 4.4-4.8).
+constexpr int kGatherWaves = 64;
+
 template <class T, int N, int RES>
 vrc_status_t launch_ar(const DropArArgs& a, int cus, hipStream_t st)
 {
     const uint64_t tiles = (a.g.nvb + 63) / 64;
-    k_dropout_allreduce<T, N, RES, 1><<<wave_grid(tiles, cus, 8), 64, 0, st>>>(a);
+    constexpr int loads = RES == 2 ? 2 * N : N + RES;
+    const int waves = allreduce_waves(loads, (loads + N) * a.g.nvb * 16);
+    k_dropout_allreduce<T, N, RES><<<wave_grid(tiles, cus, waves), 64, 0, st>>>(a);
     return check_launch();
 }
 
@@ -415,7 +440,7 @@ vrc_status_t reduce_scatter_typed(const char* const* x, const char* const* res, 
     }
     a.ch = make_chunks<T>(n, count, outer, [&](int c, uint64_t) { return (uintptr_t)y[c]; });
     a.m = m;
-    const unsigned grid = wave_grid(a.ch.tiles * (uint64_t)n, cus, 8);
+    const unsigned grid = wave_grid(a.ch.tiles * (uint64_t)n, cus, reduce_scatter_waves(n + (res ? 1 : 0), n * count * T::ESZ));
     switch (n) {
 #define VRC_CASE(N)                                                                  \
     case N:                                                                          \
@@ -443,7 +468,7 @@ vrc_status_t all_gather_typed(const char* const* x, char* const* y, int n, uint6
     const uintptr_t at = write_ref(dst, n);
     a.ch = make_chunks<T>(n, total, outer, [&](int, uint64_t off) { return at + off * T::ESZ; });
     a.m = m;
-    k_dropout_all_gather<T><<<wave_grid(a.ch.tiles * (uint64_t)n, cus, 32), 64, 0, st>>>(a);
+    k_dropout_all_gather<T><<<wave_grid(a.ch.tiles * (uint64_t)n, cus, kGatherWaves), 64, 0, st>>>(a);
     return check_launch();
 }
 
