@@ -184,32 +184,66 @@ struct ChunkArgs {
     FastDiv by_nvb[kMaxRanks];
     uint64_t rows, stride;
     uint64_t tiles;  // wave tiles per chunk (the largest chunk's)
+    uint64_t slots[kMaxRanks];  // scalar slots of each chunk
+    FastDiv by_tile;            // division of a tile's number, and of a vector's by by_nvb
     int n;
+    bool small;    // those numbers are below 2^31
+    bool scalars;  // some chunk has slots
+    // Each row's vectors start at its first element whose index is a multiple of four
+    // (else the chunk's split g puts them on the grid of its stores).  A vector off
+    // the generator's blocks of four needs one block more: twice the work in fp32.
+    bool on_blocks;
 };
+
+// Elements of a row before its vectors, on_blocks.
+__device__ __forceinline__ uint64_t before_block(const ChunkArgs& a, int c, uint64_t row)
+{
+    return (0 - (a.off[c] + row * a.stride)) & 3;
+}
 
 // Wave tile t: chunk and tile within it.  A flat split (rows == 1) walks the
 // tensor in address order; a split by columns takes the chunks in turn, so that
 // the workgroups at work read neighbouring columns of the same rows.
 __device__ __forceinline__ void tile_chunk(const ChunkArgs& a, uint64_t t, int& c, uint64_t& j)
 {
-    if (a.rows == 1) {
-        c = (int)(t / a.tiles);
-        j = t - (uint64_t)c * a.tiles;
-    } else {
-        j = t / (uint64_t)a.n;
-        c = (int)(t - j * (uint64_t)a.n);
-    }
-    c = __builtin_amdgcn_readfirstlane(c);
+    const uint64_t by = a.rows == 1 ? a.tiles : (uint64_t)a.n;
+    const uint64_t q = a.small ? a.by_tile.div((uint32_t)t) : t / by;
+    const uint64_t r = t - q * by;
+    c = __builtin_amdgcn_readfirstlane((int)(a.rows == 1 ? q : r));
+    j = a.rows == 1 ? r : q;
 }
 
-// Vector v of chunk c: its row and first column.
+// Vector v of chunk c: its row and first column; false past the row's end.
 template <class T>
-__device__ __forceinline__ void vector_place(const ChunkArgs& a, int c, uint64_t v, uint64_t& row, uint64_t& col)
+__device__ __forceinline__ bool vector_place(const ChunkArgs& a, int c, uint64_t v, uint64_t& row, uint64_t& col)
 {
     const RowSplit& g = a.g[c];
+    if (v >= a.rows * g.nvb) return false;
     row = 0;
-    if (a.rows != 1) row = (a.rows * g.nvb) >> 31 ? v / g.nvb : a.by_nvb[c].div((uint32_t)v);
-    col = g.head + (v - row * g.nvb) * T::VEC;
+    if (a.rows != 1) row = a.small ? a.by_nvb[c].div((uint32_t)v) : v / g.nvb;
+    col = (v - row * g.nvb) * T::VEC;
+    if (!a.on_blocks) {
+        col += g.head;
+        return true;
+    }
+    col += before_block(a, c, row);
+    return col + T::VEC <= a.width[c];
+}
+
+// Slot k's element of chunk c's scalars; false where it has none.
+template <class T>
+__device__ __forceinline__ bool scalar_place(const ChunkArgs& a, int c, uint64_t k, uint64_t& row, uint64_t& col)
+{
+    if (!a.on_blocks) {
+        scalar_slot(k, a.g[c], T::VEC, row, col);
+        return true;
+    }
+    constexpr uint64_t S = T::VEC + 2;
+    row = k / S;
+    const uint64_t j = k - row * S, head = before_block(a, c, row), width = a.width[c];
+    const uint64_t vectors = width > head ? (width - head) / T::VEC : 0;
+    col = j < head ? j : vectors * T::VEC + j;
+    return col < width;
 }
 
 struct DropRsArgs {
@@ -231,10 +265,8 @@ __global__ __launch_bounds__(64) void k_dropout_reduce_scatter(DropRsArgs a)
         int c;
         uint64_t j;
         tile_chunk(ch, t, c, j);
-        const uint64_t v = j * W + lane;
-        if (v >= ch.rows * ch.g[c].nvb) continue;
         uint64_t row, col;
-        vector_place<T>(ch, c, v, row, col);
+        if (!vector_place<T>(ch, c, j * W + lane, row, col)) continue;
         const uint64_t i = ch.off[c] + row * ch.stride + col;
         const uint64_t o = (row * ch.width[c] + col) * E;
         u32x4 in[N], res = {};
@@ -249,12 +281,12 @@ __global__ __launch_bounds__(64) void k_dropout_reduce_scatter(DropRsArgs a)
         for (int k = 0; k < T::VEC; k++) acc[k] = mask.apply(acc[k], bits, k);
         st16<true>(a.dst[c] + o, RES ? add_residual<T>(acc, res) : T::pack(acc));
     }
+    if (!ch.scalars) return;
     for (int c = 0; c < N; c++) {
-        const RowSplit& g = ch.g[c];
-        const uint64_t ns = ch.rows * (g.head + g.tail);
+        const uint64_t ns = ch.slots[c];
         for (uint64_t k = blockIdx.x * W + lane; k < ns; k += (uint64_t)gridDim.x * W) {
             uint64_t row, col;
-            scalar_slot(k, g, T::VEC, row, col);
+            if (!scalar_place<T>(ch, c, k, row, col)) continue;
             const uint64_t i = ch.off[c] + row * ch.stride + col;
             const uint64_t o = (row * ch.width[c] + col) * E;
             float acc = T::widen(load_s<T>(a.src[0] + i * E));
@@ -285,10 +317,8 @@ __global__ __launch_bounds__(64) void k_dropout_all_gather(DropAgArgs a)
         int c;
         uint64_t j;
         tile_chunk(ch, t, c, j);
-        const uint64_t v = j * W + lane;
-        if (v >= ch.rows * ch.g[c].nvb) continue;
         uint64_t row, col;
-        vector_place<T>(ch, c, v, row, col);
+        if (!vector_place<T>(ch, c, j * W + lane, row, col)) continue;
         const uint64_t i = ch.off[c] + row * ch.stride + col;
         const u32x4 in = ld16<true>(a.src[c] + (row * ch.width[c] + col) * E);
         const uint32_t bits = mask.keep<T::VEC>(i);
@@ -299,12 +329,12 @@ __global__ __launch_bounds__(64) void k_dropout_all_gather(DropAgArgs a)
         const u32x4 out = T::pack(x);
         for (int r = 0; r < ch.n; r++) st16<true>(a.dst[r] + i * E, out);
     }
+    if (!ch.scalars) return;
     for (int c = 0; c < ch.n; c++) {
-        const RowSplit& g = ch.g[c];
-        const uint64_t ns = ch.rows * (g.head + g.tail);
+        const uint64_t ns = ch.slots[c];
         for (uint64_t k = blockIdx.x * W + lane; k < ns; k += (uint64_t)gridDim.x * W) {
             uint64_t row, col;
-            scalar_slot(k, g, T::VEC, row, col);
+            if (!scalar_place<T>(ch, c, k, row, col)) continue;
             const uint64_t i = ch.off[c] + row * ch.stride + col;
             const float x = T::widen(load_s<T>(a.src[c] + (row * ch.width[c] + col) * E));
             const typename T::S s = T::narrow(mask.apply(x, mask.keep<1>(i), 0));
@@ -405,9 +435,10 @@ vrc_status_t allreduce_typed(const char* const* x, const char* const* res, char*
 
 // The chunks of a tensor of `total` elements split over n ranks: flat for
 // outer == 1, by columns otherwise.  `ref` gives the address that chunk c's
-// vector grid follows.
+// vector grid follows, unless `blocks` and the generator's blocks of four lie
+// otherwise.
 template <class T, class Ref>
-ChunkArgs make_chunks(int n, uint64_t total, uint64_t outer, Ref ref)
+ChunkArgs make_chunks(int n, uint64_t total, uint64_t outer, bool blocks, Ref ref)
 {
     ChunkArgs a = {};
     a.n = n;
@@ -420,11 +451,19 @@ ChunkArgs make_chunks(int n, uint64_t total, uint64_t outer, Ref ref)
             a.width[c] = a.stride / (uint64_t)n;
             a.off[c] = (uint64_t)c * a.width[c];
         }
-        a.g[c] = split_rows(ref(c, a.off[c]), a.width[c], T::ESZ);
+        a.on_blocks = a.on_blocks || (blocks && ((outer > 1 && a.stride % 4 != 0) || a.off[c] % 4 != 0));
+    }
+    for (int c = 0; c < n; c++) {
+        a.g[c] = a.on_blocks ? RowSplit{0, a.width[c] / T::VEC, 0} : split_rows(ref(c, a.off[c]), a.width[c], T::ESZ);
         a.by_nvb[c] = FastDiv::of(a.g[c].nvb);
         const uint64_t tiles = (a.rows * a.g[c].nvb + 63) / 64;
         if (tiles > a.tiles) a.tiles = tiles;
+        a.slots[c] = a.rows * (a.on_blocks ? T::VEC + 2 : a.g[c].head + a.g[c].tail);
+        a.scalars = a.scalars || a.slots[c];
     }
+    // a chunk's vectors are at most 64 of each of its tiles
+    a.small = a.tiles * 64 < 1ull << 31 && a.tiles * (uint64_t)n < 1ull << 31;
+    a.by_tile = FastDiv::of(outer == 1 ? a.tiles : (uint64_t)n);
     return a;
 }
 
@@ -438,7 +477,7 @@ vrc_status_t reduce_scatter_typed(const char* const* x, const char* const* res, 
         a.dst[r] = y[r];
         a.res[r] = res ? res[r] : nullptr;
     }
-    a.ch = make_chunks<T>(n, count, outer, [&](int c, uint64_t) { return (uintptr_t)y[c]; });
+    a.ch = make_chunks<T>(n, count, outer, true, [&](int c, uint64_t) { return (uintptr_t)y[c]; });
     a.m = m;
     const unsigned grid = wave_grid(a.ch.tiles * (uint64_t)n, cus, reduce_scatter_waves(n + (res ? 1 : 0), n * count * T::ESZ));
     switch (n) {
@@ -466,7 +505,7 @@ vrc_status_t all_gather_typed(const char* const* x, char* const* y, int n, uint6
         dst[r] = (uintptr_t)y[r];
     }
     const uintptr_t at = write_ref(dst, n);
-    a.ch = make_chunks<T>(n, total, outer, [&](int, uint64_t off) { return at + off * T::ESZ; });
+    a.ch = make_chunks<T>(n, total, outer, outer > 1, [&](int, uint64_t off) { return at + off * T::ESZ; });
     a.m = m;
     k_dropout_all_gather<T><<<wave_grid(a.ch.tiles * (uint64_t)n, cus, kGatherWaves), 64, 0, st>>>(a);
     return check_launch();
