@@ -431,9 +431,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_mx4_matmul_tiled(MatmulArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// Tiled product, large: 256 x 256 tiles, eight waves of 128 x 64, every row's
-// blocks in whole groups of G tiles (kb a multiple of 8 G, 16-byte aligned
-// scales).
+// Tiled product, large: 256 x 256 tiles, eight waves of 128 x 64.
 //
 // The waves of each half of the workgroup, one per SIMD, take turns: while one
 // half multiplies a step (256 cycles of matrix instructions), the other reads its
@@ -442,6 +440,11 @@ __global__ __launch_bounds__(WM * WN * 64) void k_mx4_matmul_tiled(MatmulArgs a)
 // into the stage that both halves have left, and have the last two steps to
 // land.  Scales come a group of G tiles ahead, 8 G bytes of a row at once, and are
 // read from LDS two tiles at a time behind the steps of the second.
+//
+// RAGGED: rows whose blocks are not whole groups of G tiles, or scales that are not
+// 16-byte aligned.  A rank's tiles are then rounded up to whole pairs (G = 2); blocks
+// past a row's end come from a constant, zero codes with scale 1, and a lane reads a
+// row's 16 scale bytes from any address and writes them to LDS itself.
 // ---------------------------------------------------------------------------
 template <int G>
 struct TurnsLds {
@@ -449,18 +452,18 @@ struct TurnsLds {
     u32x4 scales[2][512][G / 2];  // of two tiles each
 };
 
-template <class T, bool SUM, int G>
+template <class T, bool SUM, int G, bool RAGGED>
 __global__ __launch_bounds__(512) void k_mx4_matmul_turns(MatmulArgs a)
 {
     constexpr int BM = 256, BN = 256, MI = 4, NI = 2, WAVES = 8;
-    static_assert(G == 2 || G == 4, "scales of one or two pairs of tiles");
+    static_assert(G == 2 || (G == 4 && !RAGGED), "scales of one or two pairs of tiles");
     __shared__ __attribute__((aligned(16))) TurnsLds<G> lds;
 
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     uint32_t tm, tn;
     tile_of<4>(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
     const uint32_t m0 = tm * BM, n0 = tn * BN;
-    const uint32_t ktiles = a.kb / kTileBlocks;
+    const uint32_t ktiles = RAGGED ? (a.kb + 2 * kTileBlocks - 1) / (2 * kTileBlocks) * 2 : a.kb / kTileBlocks;
     const int q0 = SUM ? 0 : (int)blockIdx.y;
     const uint32_t total = ktiles * (SUM ? (uint32_t)a.ranks : 1u);
     const uint64_t row_bytes = (uint64_t)a.kb * 16;
@@ -483,6 +486,12 @@ __global__ __launch_bounds__(512) void k_mx4_matmul_turns(MatmulArgs a)
         const uint32_t row = wrow + (i * 64 + lane) / L;
         soff[i] = (row < last ? row : last) * a.kb + lane % L * 16;
     }
+    // RAGGED: this lane's row's scales on their way to LDS.  They are read at most 15
+    // bytes early, where 16 would end past the array (which holds 16 or more).
+    const uint32_t blk = place(lane / 8, lane & 7);  // this lane's block of rows 0-7; of rows 8-15, ^ 4; and so on
+    u32x4 held = {};
+    uint32_t held_skip = 0, held_left = 0, left = 0;
+    const uint64_t array_end = (isb ? a.n : a.m) * (uint64_t)a.kb - 16;
 
     // The tile that is fetched next, and the group of scales after it.
     int fq = q0;
@@ -490,6 +499,7 @@ __global__ __launch_bounds__(512) void k_mx4_matmul_turns(MatmulArgs a)
     global_ptr<const char> pcodes = nullptr, pscales = nullptr;
     const auto aim = [&] {
         live = fetched < total ? ~0u : 0u;
+        left = fkt * kTileBlocks < a.kb ? a.kb - fkt * kTileBlocks : 0;
         pcodes = (global_ptr<const char>)(isb ? a.bc[fq] : a.ac[fq]) + row0 * row_bytes + (uint64_t)fkt * kTileBytes;
     };
     const auto aim_scales = [&](int q, uint32_t kt, bool more) {
@@ -497,7 +507,33 @@ __global__ __launch_bounds__(512) void k_mx4_matmul_turns(MatmulArgs a)
         pscales = (global_ptr<const char>)(isb ? a.bs[q] : a.as[q]) + row0 * a.kb + kt * kTileBlocks;
     };
     const auto load_codes = [&](uint32_t stage, int i) {
-        load_to_lds(pcodes + opaque(off[i] & live), (u32x4*)(lds.codes[stage] + ((isb ? BM : 0) + wrow + i * 8) * kTileBytes));
+        auto from = pcodes + opaque(off[i] & live);
+        if constexpr (RAGGED)
+            if ((opaque(blk) ^ (i & 1) * 4) >= left) from = (global_ptr<const char>)&kZeroCodes;
+        load_to_lds(from, (u32x4*)(lds.codes[stage] + ((isb ? BM : 0) + wrow + i * 8) * kTileBytes));
+    };
+    const auto hold_scales = [&](int q, uint32_t kt) {
+        const uint64_t want = row0 * a.kb + soff[0] + kt * kTileBlocks, from = want < array_end ? want : array_end;
+        typedef u32x4 u32x4_at __attribute__((aligned(1)));
+        held = *(global_ptr<const u32x4_at>)((global_ptr<const char>)(isb ? a.bs[q] : a.as[q]) + from);
+        held_skip = (uint32_t)(want - from);
+        held_left = a.kb - kt * kTileBlocks;
+    };
+    const auto keep_scales = [&](uint32_t buf) {
+        uint64_t lo = (uint64_t)held.y << 32 | held.x, hi = (uint64_t)held.w << 32 | held.z;
+        const bool far = held_skip >= 8;
+        const uint32_t bits = 8 * (held_skip & 7);
+        lo = far ? hi : lo;
+        hi = far ? 0 : hi;
+        lo = lo >> bits | hi << 1 << (63 - bits);
+        hi >>= bits;
+        // bytes from held_left on are scale 1; no branches
+        const uint32_t n0 = held_left < 8 ? held_left : 8, n1 = (held_left < 16 ? held_left : 16) - n0;
+        const uint64_t gone0 = ~0ull << 4 * n0 << 4 * n0, gone1 = ~0ull << 4 * n1 << 4 * n1;
+        lo = (lo & ~gone0) | (0x7f7f7f7f7f7f7f7full & gone0);
+        hi = (hi & ~gone1) | (0x7f7f7f7f7f7f7f7full & gone1);
+        lds.scales[buf][(isb ? BM : 0) + wrow + lane][0] =
+            u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
     };
     const auto load_scales = [&](uint32_t buf, int i) {
         load_to_lds(pscales + opaque(soff[i] & slive), &lds.scales[buf][(isb ? BM : 0) + wrow][0] + i * 64);
@@ -557,16 +593,18 @@ __global__ __launch_bounds__(512) void k_mx4_matmul_turns(MatmulArgs a)
                 // the group after this one: G - 1 tiles after the tile that is fetched next
                 const uint32_t kt = fkt + (G - 1);
                 const bool more = fetched + (G - 1) < total, wrap = kt == ktiles;
-                aim_scales(fq + (more && wrap), !more || wrap ? 0 : kt, more);
+                if constexpr (RAGGED) hold_scales(fq + (more && wrap), !more || wrap ? 0 : kt);
+                else aim_scales(fq + (more && wrap), !more || wrap ? 0 : kt, more);
             }
         }
         if constexpr (k == 3) {
             advance();
             wait_vmem_below<0>();
+            if constexpr (RAGGED && g == 0) keep_scales(buf ^ 1);
         }
         meet();
         __builtin_amdgcn_s_setprio(1);
-        if constexpr (k == 0 && g == 0)
+        if constexpr (k == 0 && g == 0 && !RAGGED)
 #pragma unroll
             for (int i = 0; i < G / 2; i++) load_scales(buf ^ 1, i);
 #pragma unroll
@@ -589,11 +627,16 @@ __global__ __launch_bounds__(512) void k_mx4_matmul_turns(MatmulArgs a)
     };
 
     aim();
-    aim_scales(fq, 0, true);
 #pragma unroll
     for (int i = 0; i < 8; i++) load_codes(0, i);
+    if constexpr (RAGGED) {
+        hold_scales(fq, 0);
+        keep_scales(0);
+    } else {
+        aim_scales(fq, 0, true);
 #pragma unroll
-    for (int i = 0; i < G / 2; i++) load_scales(0, i);
+        for (int i = 0; i < G / 2; i++) load_scales(0, i);
+    }
     advance();
     wait_vmem_below<0>();
     __syncthreads();
@@ -772,14 +815,14 @@ vrc_status_t launch_tiled(MatmulArgs& a, hipStream_t st)
     return check_launch();
 }
 
-template <class T, bool SUM, int G>
+template <class T, bool SUM, int G, bool RAGGED>
 vrc_status_t launch_turns(MatmulArgs& a, hipStream_t st)
 {
     a.tiles_m = (a.m + 255) / 256;
     a.tiles_n = (a.n + 255) / 256;
     const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
     if (tiles > 0x7fffffffull) return VRC_ERR_INVALID_ARG;
-    k_mx4_matmul_turns<T, SUM, G><<<dim3((unsigned)tiles, SUM ? 1u : (unsigned)a.ranks), 512, 0, st>>>(a);
+    k_mx4_matmul_turns<T, SUM, G, RAGGED><<<dim3((unsigned)tiles, SUM ? 1u : (unsigned)a.ranks), 512, 0, st>>>(a);
     return check_launch();
 }
 
@@ -815,15 +858,17 @@ vrc_status_t launch_few(MatmulArgs a, bool swap, hipStream_t st)
 // 128 x 128 and 1.2 us with 256 x 256, whatever the grid, until the CUs are full
 // (us; 64 / 128 / 256: 256 x 8192 x 4096 12.5 / 15.0 / 24.0, 512 x 8192 x 4096
 // 23.4 / 16.7 / 25.3, 1024 x 8192 x 4096 45.7 / 25.6 / 28.1, 2048 x 8192 x 4096
-// 84.5 / 48.9 / 38.7).
+// 84.5 / 48.9 / 38.7).  Ragged rows take the same tiles: 4 x (2056 x 1000 x 4100)
+// 49 us with 256 x 256 tiles and 64 us with 544 of 128 x 128, 4096 x 8192 x 4100
+// 100 / 137 us (4096 x 8192 x 4096 76 us).
 template <class T, bool SUM>
 vrc_status_t matmul_typed(MatmulArgs& a, int cus, hipStream_t st)
 {
     const bool swap = a.n < a.m;
     const uint32_t few = swap ? a.n : a.m, many = swap ? a.m : a.n;
     const uint64_t products = SUM ? 1 : (uint64_t)a.ranks;
-    // A lane of the ragged tiles reads eight scale bytes at once, so an array has eight.
-    const bool tiny = (uint64_t)few * a.kb < 8;
+    // A lane of the ragged tiles reads up to 16 scale bytes at once, so an array has 16.
+    const bool tiny = (uint64_t)few * a.kb < 16;
     if (few <= 64 || tiny) {
         if (few > 32 && !tiny) return launch_few<T, SUM, 32, 2, 8>(a, swap, st);
         const bool by16 = ((many + 15ull) / 16) * products <= (uint64_t)cus;
@@ -836,11 +881,13 @@ vrc_status_t matmul_typed(MatmulArgs& a, int cus, hipStream_t st)
     const uint64_t room = 2 * (uint64_t)cus;
     if (!even) {
         if (tiles(64) <= room) return launch_tiled<T, SUM, false, 64, 64, 1, 2, 2>(a, st);
-        return launch_tiled<T, SUM, false, 128, 128, 2, 2, 2>(a, st);
+        // one tile a rank (kb <= 8) would be two in pairs: 8000 x 8000 x 200 34.8 us, 42.6 by pairs
+        if (tiles(128) <= room || a.kb <= kTileBlocks) return launch_tiled<T, SUM, false, 128, 128, 2, 2, 2>(a, st);
+        return launch_turns<T, SUM, 2, true>(a, st);
     }
     if (tiles(64) <= room) return launch_tiled<T, SUM, true, 64, 64, 1, 2, 4>(a, st);
     if (tiles(128) <= room) return launch_tiled<T, SUM, true, 128, 128, 2, 2, 2>(a, st);
-    return a.kb % (4 * kTileBlocks) == 0 ? launch_turns<T, SUM, 4>(a, st) : launch_turns<T, SUM, 2>(a, st);
+    return a.kb % (4 * kTileBlocks) == 0 ? launch_turns<T, SUM, 4, false>(a, st) : launch_turns<T, SUM, 2, false>(a, st);
 }
 
 }  // namespace

@@ -461,7 +461,8 @@ def test_mx4_matmul_many_ranks(vrc, n):
 
 @pytest.mark.parametrize("join,n,m,nc,k", [("sum", 1, 4001, 4100, 200), ("sum", 2, 4096, 4096, 96), ("each", 4, 2050, 1999, 300),
                                            ("sum", 3, 4001, 4100, 512), ("sum", 1, 4090, 3900, 2560), ("sum", 2, 4096, 4096, 1024),
-                                           ("each", 4, 2050, 1999, 2048), ("each", 5, 2000, 2048, 1536)])
+                                           ("each", 4, 2050, 1999, 2048), ("each", 5, 2000, 2048, 1536),
+                                           ("sum", 1, 4001, 4100, 20), ("sum", 3, 3700, 4100, 520), ("each", 6, 2050, 1999, 777)])
 def test_mx4_matmul_large_tiles(vrc, join, n, m, nc, k):
     """Enough work for the largest tiles, ragged and whole."""
     a, b = [random_mx4(m, k, r) for r in range(n)], [random_mx4(nc, k, 90 + r) for r in range(n)]
