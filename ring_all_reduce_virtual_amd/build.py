@@ -8,6 +8,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_OPS = os.path.join(PKG, "csrc_ops")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libvrc.so")
 LIB_OPS = os.path.join(PKG, "libvrc_ops.so")
@@ -17,8 +18,9 @@ SOURCES = [os.path.join(CSRC, f) for f in
            ("vrc_type_bf16.hip", "vrc_type_f16.hip", "vrc_type_f32.hip", "vrc_type_i32.hip", "vrc_api.hip")]
 # The tensor-parallel layer's operators (include/vrc_ops.h) are a library of
 # their own: libvrc.so's kernels only stream through registers, and its tests
-# pin that; these use LDS and the matrix cores.
-SOURCES_OPS = [os.path.join(CSRC, f) for f in
+# pin that; these use LDS and the matrix cores.  They have a directory of their own
+# as well: the recorded counters of libvrc.so's kernels are tied to the bytes of csrc/.
+SOURCES_OPS = [os.path.join(CSRC_OPS, f) for f in
                ("vrc_dropout.hip", "vrc_mx4_matmul.hip", "vrc_mx4.hip", "vrc_ops_api.hip")]
 OBJDIR = os.path.join(PKG, "_build")
 

@@ -11,7 +11,9 @@
 // "hcomm 的数据传输路径" section): every virtual rank lives in this GPU's HBM.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdint>
+#include <cstring>
 
 // The C ABI keeps default visibility; everything else in the library is hidden.
 #pragma GCC visibility push(default)
@@ -31,6 +33,36 @@ namespace {
 
 using namespace vrc::host;
 using vrc::kMaxRanks;
+
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_cu_count[kMaxDevices];
+
+hipError_t cu_count(int* out)
+{
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) {
+        int c = g_cu_count[dev].load(std::memory_order_relaxed);
+        if (c > 0) {
+            *out = c;
+            return hipSuccess;
+        }
+    }
+    int c = 0;
+    e = hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) return e;
+    if (c < 1) c = 1;
+    if (dev >= 0 && dev < kMaxDevices) g_cu_count[dev].store(c, std::memory_order_relaxed);
+    *out = c;
+    return hipSuccess;
+}
+
+bool overlap(uintptr_t a, uint64_t na, uintptr_t b, uint64_t nb)
+{
+    if (na == 0 || nb == 0) return false;
+    return a < b + nb && b < a + na;
+}
 
 // Validation shared by the three calls.  recv_bytes[r] is rank r's output
 // size.  allow_in_place: recv[r] == send[r] is accepted (all-reduce only).
@@ -53,6 +85,25 @@ vrc_status_t check_buffers(const void* const* send, void* const* recv, int n, ui
     return VRC_OK;
 }
 
+// Counts above 2^56 elements are rejected: every byte size computed from
+// them (at most count * 16 ranks * 4 bytes) then fits in 64 bits.
+constexpr uint64_t kMaxCount = 1ull << 56;
+
+// The enum arguments of the C ABI hold whatever int a C caller passes.  In
+// C++ an enum object whose value lies outside its enumerators' range may not
+// be read as that enum, so every entry point reads them as plain ints (from
+// the object's bytes) and the implementations check the ints before turning
+// them back into enums.
+template <class E>
+int raw(const E& e)
+{
+    static_assert(sizeof(E) == sizeof(int), "the C enums of vrc.h are int-sized");
+    int v;
+    std::memcpy(&v, &e, sizeof v);
+    return v;
+}
+
+bool dtype_valid(int d) { return d >= VRC_INT32 && d <= VRC_BF16; }
 bool mode_valid(int m) { return m >= VRC_RING && m <= VRC_TREE; }
 
 vrc_status_t check_common(const void* const* send, void* const* recv, int n, uint64_t count, int dtype)

@@ -5,10 +5,8 @@
 
 #include <hip/hip_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 #include <cstdlib>
-#include <cstring>
 #include <type_traits>
 
 #include "vrc.h"
@@ -477,59 +475,6 @@ inline vrc_status_t hip_fail(hipError_t e)
     g_last_hip_error = (int)e;
     return VRC_ERR_HIP;
 }
-
-// ----------------------------------------------------------------------------
-// Device and argument checks of the C entry points
-// ----------------------------------------------------------------------------
-constexpr int kMaxDevices = 64;
-inline std::atomic<int> g_cu_count[kMaxDevices];
-
-inline hipError_t cu_count(int* out)
-{
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevices) {
-        int c = g_cu_count[dev].load(std::memory_order_relaxed);
-        if (c > 0) {
-            *out = c;
-            return hipSuccess;
-        }
-    }
-    int c = 0;
-    e = hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev);
-    if (e != hipSuccess) return e;
-    if (c < 1) c = 1;
-    if (dev >= 0 && dev < kMaxDevices) g_cu_count[dev].store(c, std::memory_order_relaxed);
-    *out = c;
-    return hipSuccess;
-}
-
-inline bool overlap(uintptr_t a, uint64_t na, uintptr_t b, uint64_t nb)
-{
-    if (na == 0 || nb == 0) return false;
-    return a < b + nb && b < a + na;
-}
-
-// Counts above 2^56 elements are rejected: every byte size computed from
-// them (at most count * 16 ranks * 4 bytes) then fits in 64 bits.
-constexpr uint64_t kMaxCount = 1ull << 56;
-
-// The enum arguments of the C ABI hold whatever int a C caller passes.  In
-// C++ an enum object whose value lies outside its enumerators' range may not
-// be read as that enum, so every entry point reads them as plain ints (from
-// the object's bytes) and the implementations check the ints before turning
-// them back into enums.
-template <class E>
-inline int raw(const E& e)
-{
-    static_assert(sizeof(E) == sizeof(int), "the C enums of vrc.h are int-sized");
-    int v;
-    std::memcpy(&v, &e, sizeof v);
-    return v;
-}
-
-inline bool dtype_valid(int d) { return d >= VRC_INT32 && d <= VRC_BF16; }
 
 // ----------------------------------------------------------------------------
 // Element sizes, chunking, alignment split
