@@ -60,6 +60,13 @@ def ops_lib() -> C.CDLL:
     return _ops
 
 
+def _on(stream, dev: int, where: str) -> int:
+    """The HIP stream to enqueue on (see ``_stream``), which must be on the tensors' device."""
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"{where}: the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return _stream(stream, dev)
+
+
 def _done(status: int, where: str):
     if status != VRC_OK:
         raise VrcError(status, where, _ops.vrc_ops_last_hip_error())
@@ -72,10 +79,11 @@ def _pointers(tensors):
     return _POINTERS[len(tensors)](*[t.data_ptr() for t in tensors])
 
 
-# New outputs of one shape are views of one allocation while each holds at most
+# New outputs of one shape are parts of one allocation while each holds at most
 # this many bytes, in whole vectors: eight allocations cost 14 us of host time, one
-# with its views 5 us, which is what a small call takes; larger calls hide it, and
-# keep tensors that can be freed one by one.
+# with its parts 5 us, which is what a small call takes; larger calls hide it, and
+# keep tensors that can be freed one by one.  To autograd the parts are separate
+# tensors, not views of one: writing one in place leaves the others' versions alone.
 SHARED_ALLOCATION_BYTES = 4 << 20
 
 
@@ -84,8 +92,8 @@ def _allocate(shapes, dtype, device):
     first, n = shapes[0], len(shapes)
     if n > 1 and shapes.count(first) == n:
         size = _prod(first) * dtype.itemsize
-        if size <= SHARED_ALLOCATION_BYTES and size % 16 == 0:
-            return list(torch.empty((n, *first), dtype=dtype, device=device).unbind(0))
+        if first and 0 < size <= SHARED_ALLOCATION_BYTES and size % 16 == 0:
+            return list(torch.empty((n * first[0], *first[1:]), dtype=dtype, device=device).unsafe_split(first[0]))
         t0 = torch.empty(first, dtype=dtype, device=device)
         return [t0] + [torch.empty_like(t0) for _ in range(n - 1)]
     return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
@@ -168,7 +176,7 @@ def vrc_allreduce_dropout(send, p, seed, offset=0, residual=None, recv=None, str
     elif residual is not None:
         res = _pointers(_residuals(residual, shapes, send[0], where))
     drop = _dropout(p, seed, offset, send[0].device, where)
-    st = _stream(stream, dev)
+    st = _on(stream, dev, where)
     recv = _outputs(recv, shapes, send[0], where, stream)
     _done(_ops.vrc_allreduce_dropout(_pointers(send), res, _pointers(recv), n, send[0].numel(), code, C.byref(drop),
                                      st or None), where)
@@ -190,7 +198,7 @@ def vrc_reduce_scatter_dropout(send, p, seed, offset=0, residual=None, dim=0, re
     if residual is not None:
         _residuals(residual, shapes, send[0], where)
     drop = _dropout(p, seed, offset, send[0].device, where)
-    st = _stream(stream, dev)
+    st = _on(stream, dev, where)
     recv = _outputs(recv, shapes, send[0], where, stream)
     if send[0].numel() == 0:
         return recv
@@ -228,7 +236,7 @@ def vrc_all_gather_dropout(send, p, seed, offset=0, dim=0, recv=None, stream=Non
         total = _prod(shape)
     code = _float_code(send[0], where)
     drop = _dropout(p, seed, offset, send[0].device, where)
-    st = _stream(stream, dev)
+    st = _on(stream, dev, where)
     recv = _outputs(recv, [tuple(shape)] * n, send[0], where, stream)
     if total == 0:
         return recv
@@ -267,7 +275,7 @@ def vrc_mx4_quantize(x, dim=-1, codes=None, scales=None, stream=None):
         lead, kb, axis = (cols,), mx4_blocks(rows), MX4_ALONG_ROWS
     else:
         raise ValueError(f"{where}: dim must be the last dimension, or the first of a matrix")
-    st = _stream(stream, dev)
+    st = _on(stream, dev, where)
     codes = _outputs(codes, [lead + (kb * 16,)] * len(x), x[0], where, stream, torch.uint8)
     scales = _outputs(scales, [lead + (kb,)] * len(x), x[0], where, stream, torch.uint8)
     _done(_ops.vrc_mx4_quantize(_pointers(x), _pointers(codes), _pointers(scales), len(x), rows, cols, code, axis,
@@ -313,7 +321,7 @@ def vrc_mx4_dequantize(codes, scales, cols=None, dtype=None, recv=None, stream=N
     code = _out_code(dtype, where)
     lead, kb, dev = _quantised(codes, scales, where)
     cols = _decoded_cols(cols, kb, where)
-    st = _stream(stream, dev)
+    st = _on(stream, dev, where)
     recv = _outputs(recv, [lead + (cols,)] * len(codes), codes[0], where, stream, dtype)
     _done(_ops.vrc_mx4_dequantize(_pointers(codes), _pointers(scales), _pointers(recv), len(codes), _prod(lead), cols,
                                   code, st or None), where)
@@ -336,7 +344,7 @@ def vrc_mx4_all_gather(codes, scales, cols=None, dim=0, dtype=None, recv=None, s
         by_cols, shape = 0, (n * lead[0],) + lead[1:] + (cols,)
     else:
         raise ValueError(f"{where}: dim must be the first or the last dimension")
-    st = _stream(stream, dev)
+    st = _on(stream, dev, where)
     recv = _outputs(recv, [shape] * n, codes[0], where, stream, dtype)
     _done(_ops.vrc_mx4_all_gather(_pointers(codes), _pointers(scales), _pointers(recv), n, _prod(lead), cols, by_cols,
                                   code, st or None), where)
@@ -362,7 +370,7 @@ def vrc_mx4_matmul(a_codes, a_scales, b_codes, b_scales, recv=None, dtype=None, 
     lead_b, kb_b, dev_b = _quantised(b_codes, b_scales, where)
     if len(lead_b) != 1 or kb_b != kb or dev_b != dev or len(b_codes) != len(a_codes):
         raise ValueError(f"{where}: B must be a matrix per rank with A's blocks, on A's device")
-    st = _stream(stream, dev)
+    st = _on(stream, dev, where)
     recv = _outputs(recv, [lead + lead_b] * len(a_codes), a_codes[0], where, stream, dtype)
     _done(_ops.vrc_mx4_matmul(_pointers(a_codes), _pointers(a_scales), _pointers(b_codes), _pointers(b_scales),
                               _pointers(recv), len(a_codes), _prod(lead), lead_b[0], kb, code, MX4_JOINS[join],

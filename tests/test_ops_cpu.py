@@ -141,6 +141,30 @@ def test_binding_refuses_cpu_tensors_and_bad_shapes():
             ops._dropout(0.5, seed, offset, dev, "t")
 
 
+def test_binding_refuses_a_stream_of_another_device():
+    stream = type("Stream", (), {"device_index": 1, "cuda_stream": FAKE})()
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        ops._on(stream, 0, "vrc_mx4_matmul")
+
+
+@pytest.mark.parametrize("shape", [(1024,), (64, 4, 8), (8,), (3,), (0, 8), (1 << 21,)])
+def test_new_outputs_are_tensors_of_their_own(shape):
+    """One output may be written in place, also by something that needs gradients,
+    while another one is saved for a backward pass."""
+    ys = ops._allocate([shape] * 3, torch.float32, torch.device("cpu"))
+    w = torch.ones(shape, requires_grad=True)
+    assert all(y.shape == shape and y.is_contiguous() and not y._is_view() for y in ys)
+    spans = sorted((y.data_ptr(), y.data_ptr() + y.nbytes) for y in ys)
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+    for y in ys:
+        y.fill_(2)
+    loss = (w * ys[1]).sum()
+    ys[0].add_(w)
+    ys[2].zero_()
+    loss.backward()
+    assert torch.equal(w.grad, ys[1])
+
+
 def test_reference_generator_known_answers():
     """The generator's published vectors (Random123's known answers)."""
     assert [hex(w) for w in ref.philox([0], 0, 0)[0]] == ["0x6627e8d5", "0xe169c58d", "0xbc57ac4c", "0x9b00dbd8"]
