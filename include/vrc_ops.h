@@ -93,12 +93,11 @@ vrc_status_t vrc_reduce_scatter_dropout(const void* const* send, const void* con
 
 /*
  * All-gather, dropout: recv[r] = drop(concatenation of the send buffers), every
- * rank r, laid out as by vrc_all_gather (`count` elements per input viewed as
- * [outer, count / outer]); element indices are those of the gathered tensor.
- * With outer == 1 the inputs may be the chunks of a flat buffer whose length the
- * ranks do not divide: `total` is then its length, and input c holds chunk c
- * (vrc_chunk_range); else `total` is count * nranks.  For each element it is one
- * multiplication of an input, rounded once.  Outputs overlap no other buffer.
+ * rank r, laid out as by vrc_all_gather; element indices are those of the gathered
+ * tensor, which has `total` elements in `outer` rows.  With outer == 1 input c holds
+ * its chunk c (vrc_chunk_range: the last chunk takes what the ranks do not divide);
+ * with outer > 1 it holds [outer, total / outer / nranks].  For each element it is
+ * one multiplication of an input, rounded once.  Outputs overlap no other buffer.
  * Gradient: each send[c]'s is vrc_reduce_scatter_dropout of the outputs'
  * gradients (same dropout, no residual).
  */

@@ -243,7 +243,8 @@ __global__ __launch_bounds__(256) void k_mx4_quantize_t(QuantTArgs a)
     constexpr uint32_t COLS = 64 * C;
     __shared__ u32x4 out_codes[COLS][8];  // block b of column c at b ^ (c / C mod 8), against bank conflicts
     __shared__ __attribute__((aligned(8))) uint8_t out_scales[COLS][8];
-    const uint32_t tile = xcd_run(blockIdx.x, a.tiles);
+    if (wide_tile() >= a.tiles) return;
+    const uint32_t tile = xcd_run(wide_tile(), a.tiles);
     const uint64_t rt = tile / a.col_tiles, col0 = (uint64_t)(tile % a.col_tiles) * COLS;
     const uint32_t lane = threadIdx.x & 63;
     const uint64_t col = col0 + lane * C;
@@ -443,7 +444,7 @@ vrc_status_t quantize_typed(const char* const* x, char* const* codes, char* cons
         if (ct > 0x7fffffffull || ct * rt > 0x7fffffffull) return VRC_ERR_INVALID_ARG;
         a.col_tiles = (uint32_t)ct;
         a.tiles = (uint32_t)(ct * rt);
-        k_mx4_quantize_t<T><<<dim3((unsigned)(ct * rt), (unsigned)n), 256, 0, st>>>(a);
+        k_mx4_quantize_t<T><<<wide_grid(a.tiles, n), 256, 0, st>>>(a);
         return check_launch();
     }
     QuantArgs a = {};

@@ -717,7 +717,9 @@ __global__ __launch_bounds__(WAVES * 64) void k_mx4_matmul_few(MatmulArgs a)
     __shared__ float part_sum[WAVES][MI * W * (W + 1)];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t r = lane % W, part = lane / W;
-    const uint32_t n0 = blockIdx.x % a.tiles_n * W, m0 = blockIdx.x / a.tiles_n * (MI * W);
+    const uint32_t tile = wide_tile();
+    if (tile >= a.tiles_m * a.tiles_n) return;
+    const uint32_t n0 = tile % a.tiles_n * W, m0 = tile / a.tiles_n * (MI * W);
     const uint32_t ktiles = (a.kb + kTileBlocks - 1) / kTileBlocks;
     const int q0 = SUM ? 0 : (int)blockIdx.y;
     const uint32_t total = ktiles * (SUM ? (uint32_t)a.ranks : 1u);
@@ -809,7 +811,7 @@ vrc_status_t launch_tiled(MatmulArgs& a, hipStream_t st)
     a.tiles_m = (a.m + BM - 1) / BM;
     a.tiles_n = (a.n + BN - 1) / BN;
     const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
-    if (tiles > 0x7fffffffull) return VRC_ERR_INVALID_ARG;
+    if (tiles * (WM * WN * 64) > 0xffffffffull) return VRC_ERR_INVALID_ARG;  // C of 2^38 elements
     const dim3 grid((unsigned)tiles, SUM ? 1u : (unsigned)a.ranks);
     k_mx4_matmul_tiled<T, SUM, EVEN, BM, BN, WM, WN, S><<<grid, WM * WN * 64, 0, st>>>(a);
     return check_launch();
@@ -821,7 +823,7 @@ vrc_status_t launch_turns(MatmulArgs& a, hipStream_t st)
     a.tiles_m = (a.m + 255) / 256;
     a.tiles_n = (a.n + 255) / 256;
     const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
-    if (tiles > 0x7fffffffull) return VRC_ERR_INVALID_ARG;
+    if (tiles * 512 > 0xffffffffull) return VRC_ERR_INVALID_ARG;  // C of 2^39 elements
     k_mx4_matmul_turns<T, SUM, G, RAGGED><<<dim3((unsigned)tiles, SUM ? 1u : (unsigned)a.ranks), 512, 0, st>>>(a);
     return check_launch();
 }
@@ -842,10 +844,8 @@ vrc_status_t launch_few(MatmulArgs a, bool swap, hipStream_t st)
     }
     a.tiles_m = (a.m + MI * W - 1) / (MI * W);
     a.tiles_n = (a.n + W - 1) / W;
-    const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
-    if (tiles > 0x7fffffffull) return VRC_ERR_INVALID_ARG;
-    const dim3 grid((unsigned)tiles, SUM ? 1u : (unsigned)a.ranks);
-    k_mx4_matmul_few<T, SUM, W, MI, WAVES><<<grid, WAVES * 64, 0, st>>>(a);
+    static_assert(WAVES * 64 <= 512, "wide_grid's workgroups");
+    k_mx4_matmul_few<T, SUM, W, MI, WAVES><<<wide_grid((uint64_t)a.tiles_m * a.tiles_n, SUM ? 1 : a.ranks), WAVES * 64, 0, st>>>(a);
     return check_launch();
 }
 
@@ -867,15 +867,15 @@ vrc_status_t matmul_typed(MatmulArgs& a, int cus, hipStream_t st)
     const bool swap = a.n < a.m;
     const uint32_t few = swap ? a.n : a.m, many = swap ? a.m : a.n;
     const uint64_t products = SUM ? 1 : (uint64_t)a.ranks;
-    // A lane of the ragged tiles reads up to 16 scale bytes at once, so an array has 16.
-    const bool tiny = (uint64_t)few * a.kb < 16;
-    if (few <= 64 || tiny) {
-        if (few > 32 && !tiny) return launch_few<T, SUM, 32, 2, 8>(a, swap, st);
+    if (few <= 64) {
+        if (few > 32) return launch_few<T, SUM, 32, 2, 8>(a, swap, st);
         const bool by16 = ((many + 15ull) / 16) * products <= (uint64_t)cus;
-        if (few <= 16 || tiny) return by16 ? launch_few<T, SUM, 16, 1, 8>(a, swap, st) : launch_few<T, SUM, 32, 1, 8>(a, swap, st);
+        if (few <= 16) return by16 ? launch_few<T, SUM, 16, 1, 8>(a, swap, st) : launch_few<T, SUM, 32, 1, 8>(a, swap, st);
         return by16 ? launch_few<T, SUM, 16, 2, 8>(a, swap, st) : launch_few<T, SUM, 32, 1, 8>(a, swap, st);
     }
-    bool even = a.kb % (2 * kTileBlocks) == 0;
+    // From here an array of scales has 65 bytes, of which a lane of the ragged tiles
+    // reads up to 16 at once, or none (kb == 0: zeros, by the 128 x 128 tiles).
+    bool even = a.kb && a.kb % (2 * kTileBlocks) == 0;
     for (int r = 0; r < a.ranks; r++) even = even && (uintptr_t)a.as[r] % 16 == 0 && (uintptr_t)a.bs[r] % 16 == 0;
     const auto tiles = [&](uint64_t b) { return ((a.m + b - 1) / b) * ((a.n + b - 1) / b) * products; };
     const uint64_t room = 2 * (uint64_t)cus;

@@ -29,6 +29,18 @@ struct FastDiv {
     __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)(((uint64_t)n * m) >> s); }
 };
 
+// Grids of many workgroups.  A grid has less than 2^32 work items along each
+// axis, so workgroups beyond kWideX (of up to 512 lanes) go along z.  blockIdx.y is
+// the caller's; the last workgroups may have no tile.
+constexpr uint64_t kWideX = 1ull << 22;
+
+__host__ inline dim3 wide_grid(uint64_t tiles, int y)
+{
+    return dim3((unsigned)(tiles < kWideX ? tiles : kWideX), (unsigned)y, (unsigned)((tiles + kWideX - 1) / kWideX));
+}
+
+__device__ __forceinline__ uint32_t wide_tile() { return blockIdx.z * (uint32_t)kWideX + blockIdx.x; }
+
 namespace host {
 
 constexpr int kMaxDevices = 64;

@@ -494,6 +494,25 @@ def test_mx4_matmul_special_scales(vrc):
             a2, b2 = (as_.int() + sa).to(torch.uint8), (bs.int() + sb).to(torch.uint8)
             y, mag = product([ac], [a2], [bc], [b2])
             check_product(vrc.vrc_mx4_matmul([ac], [a2], [bc], [b2], dtype=torch.float32)[0], y, mag, k, "fp32", f"{sa} {sb}")
+    # a NaN scale in the largest tiles, ragged and whole
+    for k in (520, 1024):
+        (ac, as_), (bc, bs) = random_mx4(3801, k, 1), random_mx4(3900, k, 2)
+        clean = vrc.vrc_mx4_matmul([ac], [as_], [bc], [bs], dtype=torch.float32)[0].clone()
+        as_[3800, 1], bs[7, 5] = 255, 255
+        y = vrc.vrc_mx4_matmul([ac], [as_], [bc], [bs], dtype=torch.float32)[0]
+        bad = torch.zeros_like(y, dtype=torch.bool)
+        bad[3800, :], bad[:, 7] = True, True
+        assert torch.equal(torch.isnan(y), bad) and torch.equal(y[~bad], clean[~bad])
+    # the ends of the scales' range: sums of these are whole multiples of their smallest
+    # product and below 2^24 of them, so fp32 holds them exactly while they are in its range
+    for m, nc, k in ((1, 40, 96), (70, 130, 512), (300, 300, 90)):
+        (ac, _), (bc, _) = random_mx4(m, k, 8), random_mx4(nc, k, 9)
+        for ea, eb in ((252, 2), (2, 252), (0, 252), (254, 0), (0, 127), (64, 60), (0, 110), (0, 0)):
+            sa = torch.full((m, -(-k // 32)), ea, dtype=torch.uint8, device=DEV)
+            sb = torch.full((nc, -(-k // 32)), eb, dtype=torch.uint8, device=DEV)
+            y, _ = product([ac], [sa], [bc], [sb])
+            got = f64(vrc.vrc_mx4_matmul([ac], [sa], [bc], [sb], dtype=torch.float32)[0])
+            assert (got == y.astype(np.float32)).all(), (ea, eb)
     none = torch.empty(5, 0, dtype=torch.uint8, device=DEV)
     assert not vrc.vrc_mx4_matmul([none], [none], [none[:3]], [none[:3]])[0].any()
 
@@ -522,6 +541,37 @@ def test_mx4_past_32_bits(vrc):
     last = rows - 3  # the last block's three rows
     want, want_s = ref.quantise(f64(x[last:]).T[-64:])
     assert (ref.unpack(tcodes[0][-64:, -16:].cpu().numpy()) == want).all() and (tscales[0][-64:, -1:].cpu().numpy() == want_s).all()
+
+
+def test_mx4_more_workgroups_than_a_grid_axis_holds(vrc):
+    """2^32 work items along one axis of a grid: thin matrices reach them first."""
+    rows = (1 << 32) + 300
+    x = torch.empty(rows, dtype=torch.bfloat16, device=DEV)
+    x[: 1 << 31].normal_()
+    x[1 << 31:].normal_()
+    down = vrc.vrc_mx4_quantize([x.view(rows, 1)], dim=0)
+    along = vrc.vrc_mx4_quantize([x.view(1, rows)])
+    assert torch.equal(down[0][0].view(-1), along[0][0].view(-1))
+    assert torch.equal(down[1][0].view(-1), along[1][0].view(-1))
+    del x, down, along
+    # one row by 2^27 + 5: a period of B's rows is one of the product
+    period, rows = 1 << 20, (1 << 27) + 5
+    (ac, as_), (bc, bs) = random_mx4(1, 32, 41), random_mx4(period, 32, 42)
+    times = -(-rows // period)
+    wide = [t.repeat(times, 1)[:rows].contiguous() for t in (bc, bs)]
+    y = torch.full((1, rows), -1.0, dtype=torch.float32, device=DEV)
+    vrc.vrc_mx4_matmul([ac], [as_], [wide[0]], [wide[1]], recv=[y], dtype=torch.float32)
+    one = vrc.vrc_mx4_matmul([ac], [as_], [bc], [bs], dtype=torch.float32)[0]
+    assert torch.equal(y, one.repeat(1, times)[:, :rows])
+    yt = torch.full((rows, 1), -1.0, dtype=torch.float32, device=DEV)
+    vrc.vrc_mx4_matmul([wide[0]], [wide[1]], [ac], [as_], recv=[yt], dtype=torch.float32)
+    assert torch.equal(yt.view(-1), y.view(-1))
+    del wide, y, yt
+    # nothing to contract: zeros, however many of them
+    none = [torch.empty(70000, k, dtype=torch.uint8, device=DEV) for k in (0, 0)]
+    z = torch.full((70000, 70000), -1.0, dtype=torch.bfloat16, device=DEV)
+    vrc.vrc_mx4_matmul([none[0]], [none[1]], [none[0]], [none[1]], recv=[z])
+    assert not z.view(torch.int16).any()
 
 
 # ---------------------------------------------------------------------------
