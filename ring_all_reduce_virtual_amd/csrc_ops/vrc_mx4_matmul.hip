@@ -15,7 +15,7 @@
 // each tile); 8192 x 8192 x 8192 253 us (4.34).  The matrix instructions alone,
 // operands from LDS but nothing loaded, take 213 us: random operands hold the
 // clock down (205 us whole on zeros), and 41 us of either are tile starts and
-// ends.  1 x 8192 x 8 x 4096, a stream of 143 MB: 26 us, 5.5 TB/s.
+// ends.  8 x (1 x 8192 x 4096) summed, a stream of 143 MB: 30.5 us, 4.7 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <utility>
@@ -43,7 +43,8 @@ struct MatmulArgs {
     uint32_t m, n, kb;
     int ranks;
     uint32_t tiles_m, tiles_n;
-    uint64_t sm, sn;  // strides of C's rows and columns (the few-rows kernel)
+    uint64_t sm, sn;  // strides of C's rows and columns, and division by a row's
+    FastDiv by_ktiles;  // tiles (the few-rows kernel)
 };
 
 // acc += the 64 products per output of step S (blocks 2S and 2S + 1) of a tile;
@@ -63,15 +64,16 @@ __device__ __forceinline__ uint32_t step_scales(u32x2 bytes, uint32_t half)
     return __builtin_amdgcn_perm(bytes.y, bytes.x, half ? 0x07050301u : 0x06040200u);
 }
 
-// A row's eight scale bytes of the tile at `p`, or the `left` that it has and 127
-// (scale 1) for the rest.
-__device__ __forceinline__ u32x2 row_of_scales(const char* p, uint32_t left)
+// What a block past the end of a row is read from.
+__device__ const u32x4 kZeroCodes = {0, 0, 0, 0};
+
+// `x`, whose origin the compiler is not to see: an address is then a uniform base
+// and a 32-bit lane offset, which a load takes as they are, instead of a 64-bit
+// address per lane and load kept in registers over the whole loop.
+__device__ __forceinline__ uint32_t opaque(uint32_t x)
 {
-    if (left >= kTileBlocks) return *(global_ptr<const u32x2_any>)p;
-    uint64_t v = 0x7f7f7f7f7f7f7f7full;
-    for (uint32_t i = 0; i < left; i++)
-        v = (v & ~(0xffull << (8 * i))) | (uint64_t)*(global_ptr<const uint8_t>)(p + i) << (8 * i);
-    return u32x2{(uint32_t)v, (uint32_t)(v >> 32)};
+    __asm__ volatile("" : "+v"(x));
+    return x;
 }
 
 // Four consecutive columns, rounded.
@@ -160,8 +162,6 @@ __device__ __forceinline__ void store_results(const MatmulArgs& a, const f32x16 
 // number of loads under way, which is what its waits count; and with a branch the
 // compiler moves the matrix instructions behind it, all four steps' operands live.
 // ---------------------------------------------------------------------------
-__device__ const u32x4 kZeroCodes = {0, 0, 0, 0};
-
 __device__ __forceinline__ uint32_t place(uint32_t row, uint32_t block) { return block ^ (row >> 1 & 7); }
 
 // A barrier behind this wave's LDS reads and writes, with its direct loads left
@@ -205,15 +205,6 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t tiles_m, uint32_t t
     const uint32_t i = t - group * G * tiles_n;
     tm = group * G + i % rows;
     tn = i / rows;
-}
-
-// `x`, whose origin the compiler is not to see: an address is then a uniform base
-// and a 32-bit lane offset, which a load takes as they are, instead of a 64-bit
-// address per lane and load kept in registers over the whole loop.
-__device__ __forceinline__ uint32_t opaque(uint32_t x)
-{
-    __asm__ volatile("" : "+v"(x));
-    return x;
 }
 
 template <class T, bool SUM, bool EVEN, int BM, int BN, int WM, int WN, int S>
@@ -665,8 +656,8 @@ __global__ __launch_bounds__(512) void k_mx4_matmul_turns(MatmulArgs a)
 // Few rows of one operand, A here: a stream of the other.  A workgroup has W (32
 // or 16) columns of C (rows of B) and MI x W of its rows; its waves take the
 // contraction's tiles in turn, straight from memory into registers, the next
-// tile's loads in flight while one is multiplied, and the waves' sums meet in LDS,
-// added in wave order.
+// two tiles' loads in flight while one is multiplied, and the waves' sums meet in
+// LDS, added in wave order.
 // ---------------------------------------------------------------------------
 template <int W>
 struct Wide;
@@ -674,10 +665,14 @@ template <>
 struct Wide<32> {
     typedef f32x16 Acc;
     static constexpr int STEPS = 4;
-    // A lane's scales of a tile's steps, from its row's eight bytes.
+    // A lane's scales of a tile's steps, from its row's eight bytes, or from its own.
     __device__ static void scales(u32x2 bytes, uint32_t part, uint32_t* s)
     {
         s[0] = s[1] = s[2] = s[3] = step_scales(bytes, part);
+    }
+    __device__ static void own_scales(const uint32_t* bytes, uint32_t* s)
+    {
+        s[0] = s[1] = s[2] = s[3] = bytes[0] | bytes[1] << 8 | bytes[2] << 16 | bytes[3] << 24;
     }
     template <int S>
     __device__ static Acc mul(u32x4 b, u32x4 a, Acc acc, uint32_t sb, uint32_t sa) { return mfma<S>(b, a, acc, sb, sa); }
@@ -693,6 +688,11 @@ struct Wide<16> {
         s[0] = bytes.x >> (8 * part);
         s[1] = bytes.y >> (8 * part);
     }
+    __device__ static void own_scales(const uint32_t* bytes, uint32_t* s)
+    {
+        s[0] = bytes[0];
+        s[1] = bytes[1];
+    }
     template <int S>
     __device__ static Acc mul(u32x4 b, u32x4 a, Acc acc, uint32_t sb, uint32_t sa)
     {
@@ -703,17 +703,63 @@ struct Wide<16> {
     __device__ static uint32_t col(int e, uint32_t part) { return 4 * part + e; }
 };
 
-template <int W, int MI>
-struct Frag {
-    u32x4 b[Wide<W>::STEPS], a[MI][Wide<W>::STEPS];
-    u32x2 sb, sa[MI];
+// A lane's part of a row of a tile: the blocks that it multiplies, and their scales.
+// WHOLE: rows are whole tiles, and a row's eight scales are read at once.  Else a lane
+// reads the bytes of its own blocks; a block past the row's end comes from a
+// constant, zero codes, and has scale 1.
+template <int W, bool WHOLE>
+struct RowPart {
+    static constexpr int STEPS = Wide<W>::STEPS, PARTS = 64 / W;
+    u32x4 codes[STEPS];
+    u32x2 scales;             // WHOLE
+    uint32_t bytes[STEPS];    // else
+
+    // codes and scales: of the tile's first row, at this tile; off: the row's offset in
+    // scale bytes (in codes 16 times that); left: blocks that the tile has.
+    __device__ __forceinline__ void load(global_ptr<const char> c, global_ptr<const char> sc, uint32_t off,
+                                         uint32_t part, uint32_t left)
+    {
+        const auto at = c + opaque((off + part) * 16);
+#pragma unroll
+        for (int s = 0; s < STEPS; s++) {
+            auto from = at + (PARTS * 16 * s);
+            if constexpr (!WHOLE) from = PARTS * s + part < left ? from : (global_ptr<const char>)&kZeroCodes;
+            codes[s] = *(global_ptr<const u32x4>)from;
+        }
+        if constexpr (WHOLE) {
+            scales = *(global_ptr<const u32x2_any>)(sc + opaque(off));
+        } else {
+#pragma unroll
+            for (int s = 0; s < STEPS; s++) {
+                const uint32_t b = PARTS * s + part;
+                bytes[s] = *(global_ptr<const uint8_t>)(sc + opaque(off + (b < left ? b : left - 1)));
+            }
+        }
+    }
+    __device__ __forceinline__ void steps(uint32_t part, uint32_t left, uint32_t* s) const
+    {
+        if constexpr (WHOLE) {
+            Wide<W>::scales(scales, part, s);
+        } else {
+            uint32_t b[STEPS];
+#pragma unroll
+            for (int i = 0; i < STEPS; i++) b[i] = PARTS * i + part < left ? bytes[i] : 127u;
+            Wide<W>::own_scales(b, s);
+        }
+    }
 };
 
-template <class T, bool SUM, int W, int MI, int WAVES>
+template <int W, int MI, bool WHOLE>
+struct Frag {
+    RowPart<W, WHOLE> b, a[MI];
+    uint32_t left;  // blocks that the tile has
+};
+
+template <class T, bool SUM, bool WHOLE, int W, int MI, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void k_mx4_matmul_few(MatmulArgs a)
 {
     typedef Wide<W> Op;
-    constexpr int STEPS = Op::STEPS, PARTS = 64 / W, RESULTS = W * W / 64;
+    constexpr int STEPS = Op::STEPS, RESULTS = W * W / 64;
     __shared__ float part_sum[WAVES][MI * W * (W + 1)];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t r = lane % W, part = lane / W;
@@ -723,67 +769,67 @@ __global__ __launch_bounds__(WAVES * 64) void k_mx4_matmul_few(MatmulArgs a)
     const uint32_t ktiles = (a.kb + kTileBlocks - 1) / kTileBlocks;
     const int q0 = SUM ? 0 : (int)blockIdx.y;
     const uint32_t total = ktiles * (SUM ? (uint32_t)a.ranks : 1u);
-    const uint64_t rb = n0 + r < a.n ? n0 + r : a.n - 1;
-    uint64_t ra[MI];
+    // Rows past the end read the last one again.
+    const uint32_t last_b = a.n - 1 - n0, last_a = a.m - 1 - m0;
+    const uint32_t off_b = (r < last_b ? r : last_b) * a.kb;
+    uint32_t off_a[MI];
 #pragma unroll
-    for (int i = 0; i < MI; i++) ra[i] = m0 + i * W + r < a.m ? m0 + i * W + r : a.m - 1;
+    for (int i = 0; i < MI; i++) off_a[i] = (i * W + r < last_a ? i * W + r : last_a) * a.kb;
 
-    const auto fetch = [&](Frag<W, MI>& f, uint32_t t) {
-        const uint32_t qi = t / ktiles, kt = t - qi * ktiles;
+    const auto fetch = [&](Frag<W, MI, WHOLE>& f, uint32_t t) {
+        const uint32_t qi = a.by_ktiles.div(t), kt = t - qi * ktiles;
         const int q = q0 + (int)qi;
-        const uint64_t k0 = (uint64_t)kt * kTileBlocks;
-        const uint32_t left = a.kb - kt * kTileBlocks;
-        f.sb = row_of_scales(a.bs[q] + rb * a.kb + k0, left);
+        const uint64_t k0 = (uint64_t)kt * kTileBlocks, at_b = (uint64_t)n0 * a.kb + k0, at_a = (uint64_t)m0 * a.kb + k0;
+        f.left = a.kb - kt * kTileBlocks;
+        f.b.load((global_ptr<const char>)a.bc[q] + at_b * 16, (global_ptr<const char>)a.bs[q] + at_b, off_b, part, f.left);
 #pragma unroll
-        for (int i = 0; i < MI; i++) f.sa[i] = row_of_scales(a.as[q] + ra[i] * a.kb + k0, left);
-        const char* pb = a.bc[q] + (rb * a.kb + k0 + part) * 16;
-        if (left >= kTileBlocks) {
-#pragma unroll
-            for (int s = 0; s < STEPS; s++) f.b[s] = *(global_ptr<const u32x4>)(pb + PARTS * 16 * s);
-#pragma unroll
-            for (int i = 0; i < MI; i++) {
-                const char* pa = a.ac[q] + (ra[i] * a.kb + k0 + part) * 16;
-#pragma unroll
-                for (int s = 0; s < STEPS; s++) f.a[i][s] = *(global_ptr<const u32x4>)(pa + PARTS * 16 * s);
-            }
-        } else {
-#pragma unroll
-            for (int s = 0; s < STEPS; s++)
-                f.b[s] = PARTS * s + part < left ? *(global_ptr<const u32x4>)(pb + PARTS * 16 * s) : u32x4{};
-#pragma unroll
-            for (int i = 0; i < MI; i++) {
-                const char* pa = a.ac[q] + (ra[i] * a.kb + k0 + part) * 16;
-#pragma unroll
-                for (int s = 0; s < STEPS; s++)
-                    f.a[i][s] = PARTS * s + part < left ? *(global_ptr<const u32x4>)(pa + PARTS * 16 * s) : u32x4{};
-            }
-        }
+        for (int i = 0; i < MI; i++)
+            f.a[i].load((global_ptr<const char>)a.ac[q] + at_a * 16, (global_ptr<const char>)a.as[q] + at_a, off_a[i], part,
+                        f.left);
     };
     typename Op::Acc acc[MI] = {};
-    const auto multiply = [&](const Frag<W, MI>& f) {
+    const auto multiply = [&](const Frag<W, MI, WHOLE>& f) {
         uint32_t sb[STEPS];
-        Op::scales(f.sb, part, sb);
+        f.b.steps(part, f.left, sb);
 #pragma unroll
         for (int i = 0; i < MI; i++) {
             uint32_t sa[STEPS];
-            Op::scales(f.sa[i], part, sa);
-            acc[i] = Op::template mul<0>(f.b[0], f.a[i][0], acc[i], sb[0], sa[0]);
-            acc[i] = Op::template mul<1>(f.b[1], f.a[i][1], acc[i], sb[1], sa[1]);
+            f.a[i].steps(part, f.left, sa);
+            acc[i] = Op::template mul<0>(f.b.codes[0], f.a[i].codes[0], acc[i], sb[0], sa[0]);
+            acc[i] = Op::template mul<1>(f.b.codes[1], f.a[i].codes[1], acc[i], sb[1], sa[1]);
             if constexpr (STEPS == 4) {
-                acc[i] = Op::template mul<2>(f.b[2], f.a[i][2], acc[i], sb[2], sa[2]);
-                acc[i] = Op::template mul<3>(f.b[3], f.a[i][3], acc[i], sb[3], sa[3]);
+                acc[i] = Op::template mul<2>(f.b.codes[2], f.a[i].codes[2], acc[i], sb[2], sa[2]);
+                acc[i] = Op::template mul<3>(f.b.codes[3], f.a[i].codes[3], acc[i], sb[3], sa[3]);
             }
         }
     };
-    Frag<W, MI> f0, f1;
-    uint32_t t = wave;
-    if (t < total) fetch(f0, t);
-    for (; t < total; t += 2 * WAVES) {
-        if (t + WAVES < total) fetch(f1, t + WAVES);
-        multiply(f0);
-        if (t + WAVES >= total) break;
-        if (t + 2 * WAVES < total) fetch(f0, t + 2 * WAVES);
-        multiply(f1);
+    // Two tiles ahead, without a branch around the loads: where some may not be under
+    // way, the compiler waits for all of them before each product (8 x (1 x 8192 x
+    // 4096) 32.5 us instead of 30.5, 4 x (1 x 5120 x 640) 5.3 instead of 4.3).  Three
+    // tiles ahead or 16 waves gain nothing; loads that pass by the caches take 46 us,
+    // as a row's line is read in four pieces.
+    Frag<W, MI, WHOLE> f[2];
+    uint32_t t = wave, left = t < total ? (total - t + WAVES - 1) / WAVES : 0;
+    const auto turn = [&](int d) {
+        multiply(f[d]);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(f[d], t + (2 + d) * WAVES);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (left >= 2) {
+        fetch(f[0], t);
+        fetch(f[1], t + WAVES);
+        for (; left >= 4; left -= 2, t += 2 * WAVES) {
+            turn(0);
+            turn(1);
+        }
+        if (left == 3) turn(0);
+        else multiply(f[0]);
+        multiply(f[1]);
+        if (left == 3) multiply(f[0]);
+    } else if (left) {
+        fetch(f[0], t);
+        multiply(f[0]);
     }
 #pragma unroll
     for (int i = 0; i < MI; i++)
@@ -844,16 +890,19 @@ vrc_status_t launch_few(MatmulArgs a, bool swap, hipStream_t st)
     }
     a.tiles_m = (a.m + MI * W - 1) / (MI * W);
     a.tiles_n = (a.n + W - 1) / W;
-    static_assert(WAVES * 64 <= 512, "wide_grid's workgroups");
-    k_mx4_matmul_few<T, SUM, W, MI, WAVES><<<wide_grid((uint64_t)a.tiles_m * a.tiles_n, SUM ? 1 : a.ranks), WAVES * 64, 0, st>>>(a);
+    static_assert(WAVES * 64 <= 1024, "wide_grid's workgroups");
+    a.by_ktiles = FastDiv::of((a.kb + kTileBlocks - 1) / kTileBlocks);
+    const dim3 grid = wide_grid((uint64_t)a.tiles_m * a.tiles_n, SUM ? 1 : a.ranks);
+    if (a.kb % kTileBlocks == 0) k_mx4_matmul_few<T, SUM, true, W, MI, WAVES><<<grid, WAVES * 64, 0, st>>>(a);
+    else k_mx4_matmul_few<T, SUM, false, W, MI, WAVES><<<grid, WAVES * 64, 0, st>>>(a);
     return check_launch();
 }
 
 // The kernel by sizes.  One operand of up to 64 rows: a stream of the other, by 16
 // columns where that makes at most a workgroup per CU and by 32 otherwise (us; 16 /
-// 32 columns: 1 x 4096 x 16384 9.5 / 14.0, 32 x 4096 x 16384 18.5 / 20.6; but
-// 1 x 8192 x 8 x 4096 29.6 / 26.5, 32 x 8192 x 4096 10.4 / 7.5, and from 33 rows
-// 48 x 5003 x 4 x 1000 14.5 / 9.6).  Else the smallest tiles of which at most two a CU
+// 32 columns: 1 x 4096 x 16384 9.9 / 13.9, 32 x 4096 x 16384 19.1 / 20.6, 8 x (7 x
+// 4096 x 2048) 10.4 / 14.5; but 8 x (1 x 8192 x 4096) 33.8 / 31.0, 32 x 8192 x 4096
+// 11.2 / 7.9, and from 33 rows 4 x (48 x 5003 x 1000) 14.5 / 9.5).  Else the smallest tiles of which at most two a CU
 // are needed: a tile of the contraction takes 0.5 us with 64 x 64 tiles, 0.7 us with
 // 128 x 128 and 1.2 us with 256 x 256, whatever the grid, until the CUs are full
 // (us; 64 / 128 / 256: 256 x 8192 x 4096 12.5 / 15.0 / 24.0, 512 x 8192 x 4096

@@ -30,9 +30,9 @@ struct FastDiv {
 };
 
 // Grids of many workgroups.  A grid has less than 2^32 work items along each
-// axis, so workgroups beyond kWideX (of up to 512 lanes) go along z.  blockIdx.y is
+// axis, so workgroups beyond kWideX (of up to 1024 lanes) go along z.  blockIdx.y is
 // the caller's; the last workgroups may have no tile.
-constexpr uint64_t kWideX = 1ull << 22;
+constexpr uint64_t kWideX = 1ull << 21;
 
 __host__ inline dim3 wide_grid(uint64_t tiles, int y)
 {
