@@ -304,6 +304,23 @@ def test_quantise_both_axes(vrc, dtype, shape):
         assert torch.equal(y.cpu(), want.to(torch.float32).to(DT[dtype]))
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("shape", [(256, 131), (500, 70), (225, 1), (1024, 260)])
+def test_quantise_down_columns_in_whole_lines(vrc, dtype, shape):
+    """Eight blocks of a column fill a memory line; codes on a line and 16 bytes off it."""
+    xs = workloads.random_ranks(2, shape, dtype, seed=90, device=DEV)
+    kb = -(-shape[0] // 32)
+    room = [torch.full((shape[1] * kb * 16 + 32,), 0xA5, dtype=torch.uint8, device=DEV) for _ in xs]
+    off = [t[16:-16].view(shape[1], kb * 16) for t in room]
+    on_line = vrc.vrc_mx4_quantize(xs, dim=0)
+    moved = vrc.vrc_mx4_quantize(xs, dim=0, codes=off)
+    for x, c, s, c2, s2, t in zip(xs, *on_line, *moved, room):
+        codes, scales = ref.quantise(f64(x).T)
+        assert (ref.unpack(c.cpu().numpy()) == codes).all() and (s.cpu().numpy() == scales).all()
+        assert torch.equal(c, c2) and torch.equal(s, s2)
+        assert (t[:16] == 0xA5).all() and (t[-16:] == 0xA5).all()
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 def test_quantise_every_16_bit_value(vrc, dtype):
     """Each finite value beside block maxima of every exponent from its own upwards."""
