@@ -10,8 +10,10 @@ from __future__ import annotations
 import ctypes as C
 import os
 
-from . import (MAX_RANKS, PKG, VRC_BF16, VRC_FP16, VRC_FP32, VRC_OK, VrcError, _check_ranks, _dtype_code, _outer,
-               _prod, _stream, _torch, chunk_range, reduce_scatter_shape)
+from math import prod as _prod
+
+from . import (MAX_RANKS, PKG, VRC_BF16, VRC_FP16, VRC_FP32, VRC_OK, VrcError, _check_ranks, _outer, _stream, _torch,
+               reduce_scatter_shape)
 
 OPS_LIB_PATH = os.path.join(PKG, "libvrc_ops.so")
 OPS_VERSION = 100  # VRC_OPS_VERSION of include/vrc_ops.h that this binding follows
@@ -90,13 +92,12 @@ SHARED_ALLOCATION_BYTES = 4 << 20
 def _allocate(shapes, dtype, device):
     torch = _torch()
     first, n = shapes[0], len(shapes)
-    if n > 1 and shapes.count(first) == n:
-        size = _prod(first) * dtype.itemsize
-        if first and 0 < size <= SHARED_ALLOCATION_BYTES and size % 16 == 0:
-            return list(torch.empty((n * first[0], *first[1:]), dtype=dtype, device=device).unsafe_split(first[0]))
-        t0 = torch.empty(first, dtype=dtype, device=device)
-        return [t0] + [torch.empty_like(t0) for _ in range(n - 1)]
-    return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
+    size = _prod(first) * dtype.itemsize
+    if n > 1 and first and 0 < size <= SHARED_ALLOCATION_BYTES and size % 16 == 0 and shapes.count(first) == n:
+        return list(torch.empty((n * first[0], *first[1:]), dtype=dtype, device=device).unsafe_split(first[0]))
+    t0 = torch.empty(first, dtype=dtype, device=device)
+    return [t0] + [torch.empty_like(t0) if s == first else torch.empty(s, dtype=dtype, device=device)
+                   for s in shapes[1:]]
 
 
 def _outputs(recv, shapes, like, where, stream, dtype=None):
@@ -121,11 +122,22 @@ def _outputs(recv, shapes, like, where, stream, dtype=None):
     return recv
 
 
-def _float_code(t, where) -> int:
-    code = _dtype_code(t)
-    if code not in (VRC_FP32, VRC_FP16, VRC_BF16):
-        raise TypeError(f"{where}: unsupported dtype {t.dtype}")
+_CODES: dict = {}  # torch dtype -> vrc_dtype_t, filled by the first call
+
+
+def _float_code(dtype, where) -> int:
+    if not _CODES:
+        torch = _torch()
+        _CODES.update({torch.float32: VRC_FP32, torch.float16: VRC_FP16, torch.bfloat16: VRC_BF16})
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{where}: unsupported dtype {dtype}")
     return code
+
+
+def _chunk_sizes(count: int, n: int) -> list:
+    """The lengths of vrc_chunk_range's chunks: equal ones, the last with the remainder."""
+    return [count // n] * (n - 1) + [count - (n - 1) * (count // n)]
 
 
 def _dropout(p, seed, offset, device, where) -> Dropout:
@@ -146,8 +158,9 @@ def _dropout(p, seed, offset, device, where) -> Dropout:
 def _residuals(residual, shapes, like, where):
     if not isinstance(residual, (list, tuple)) or len(residual) != len(shapes):
         raise ValueError(f"{where}: one residual per rank")
+    dtype, at = like.dtype, like.get_device()
     for c, (t, s) in enumerate(zip(residual, shapes)):
-        if t.numel() != _prod(s) or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
+        if t.numel() != _prod(s) or t.dtype is not dtype or t.get_device() != at or not t.is_contiguous():
             raise ValueError(f"{where}: residual {c} must be contiguous {tuple(s)} {like.dtype} on {like.device}")
     return residual
 
@@ -165,7 +178,7 @@ def vrc_allreduce_dropout(send, p, seed, offset=0, residual=None, recv=None, str
     where = "vrc_allreduce_dropout"
     torch = _torch()
     dev = _check_ranks(send, where)
-    code = _float_code(send[0], where)
+    code = _float_code(send[0].dtype, where)
     n = len(send)
     shape = tuple(send[0].shape)
     shapes = [shape] * n
@@ -192,9 +205,10 @@ def vrc_reduce_scatter_dropout(send, p, seed, offset=0, residual=None, dim=0, re
     outputs' gradients with the same (p, seed, offset)."""
     where = "vrc_reduce_scatter_dropout"
     dev = _check_ranks(send, where)
-    code = _float_code(send[0], where)
+    code = _float_code(send[0].dtype, where)
     outer, _ = _outer(send[0].shape, dim)
-    shapes = reduce_scatter_shape(tuple(send[0].shape), len(send), dim)
+    n, shape = len(send), tuple(send[0].shape)
+    shapes = [(k,) for k in _chunk_sizes(_prod(shape), n)] if outer == 1 else reduce_scatter_shape(shape, n, dim)
     if residual is not None:
         _residuals(residual, shapes, send[0], where)
     drop = _dropout(p, seed, offset, send[0].device, where)
@@ -203,7 +217,7 @@ def vrc_reduce_scatter_dropout(send, p, seed, offset=0, residual=None, dim=0, re
     if send[0].numel() == 0:
         return recv
     _done(_ops.vrc_reduce_scatter_dropout(_pointers(send), None if residual is None else _pointers(residual),
-                                          _pointers(recv), len(send), send[0].numel(), outer, code, C.byref(drop),
+                                          _pointers(recv), n, send[0].numel(), outer, code, C.byref(drop),
                                           st or None), where)
     return recv
 
@@ -222,7 +236,7 @@ def vrc_all_gather_dropout(send, p, seed, offset=0, dim=0, recv=None, stream=Non
         dev = _check_ranks(send[:-1], where)
         _check_ranks(send[-1:], where)
         total = sum(t.numel() for t in send)
-        if [t.numel() for t in send] != [chunk_range(total, n, c)[1] for c in range(n)]:
+        if [t.numel() for t in send] != _chunk_sizes(total, n):
             raise ValueError(f"{where}: uneven inputs must be the chunks of a flat tensor, the last with the remainder")
         if send[-1].dtype != send[0].dtype or send[-1].device != send[0].device:
             raise ValueError(f"{where}: all ranks need the same dtype and device")
@@ -234,7 +248,7 @@ def vrc_all_gather_dropout(send, p, seed, offset=0, dim=0, recv=None, stream=Non
         shape = list(send[0].shape)
         shape[d] *= n
         total = _prod(shape)
-    code = _float_code(send[0], where)
+    code = _float_code(send[0].dtype, where)
     drop = _dropout(p, seed, offset, send[0].device, where)
     st = _on(stream, dev, where)
     recv = _outputs(recv, [tuple(shape)] * n, send[0], where, stream)
@@ -263,7 +277,7 @@ def vrc_mx4_quantize(x, dim=-1, codes=None, scales=None, stream=None):
     where = "vrc_mx4_quantize"
     torch = _torch()
     dev = _check_ranks(x, where)
-    code = _float_code(x[0], where)
+    code = _float_code(x[0].dtype, where)
     shape = tuple(x[0].shape)
     if not shape:
         raise ValueError("tensors need at least one dimension")
@@ -304,21 +318,13 @@ def _decoded_cols(cols, kb, where) -> int:
     return cols
 
 
-def _out_code(dtype, where) -> int:
-    torch = _torch()
-    codes = {torch.float32: VRC_FP32, torch.float16: VRC_FP16, torch.bfloat16: VRC_BF16}
-    if dtype not in codes:
-        raise TypeError(f"{where}: unsupported dtype {dtype}")
-    return codes[dtype]
-
-
 def vrc_mx4_dequantize(codes, scales, cols=None, dtype=None, recv=None, stream=None):
     """recv[r] = the [..., cols] values of rank r's codes (``cols=None``: whole
     blocks), in ``dtype`` (default bfloat16)."""
     where = "vrc_mx4_dequantize"
     torch = _torch()
     dtype = torch.bfloat16 if dtype is None else dtype
-    code = _out_code(dtype, where)
+    code = _float_code(dtype, where)
     lead, kb, dev = _quantised(codes, scales, where)
     cols = _decoded_cols(cols, kb, where)
     st = _on(stream, dev, where)
@@ -334,7 +340,7 @@ def vrc_mx4_all_gather(codes, scales, cols=None, dim=0, dtype=None, recv=None, s
     where = "vrc_mx4_all_gather"
     torch = _torch()
     dtype = torch.bfloat16 if dtype is None else dtype
-    code = _out_code(dtype, where)
+    code = _float_code(dtype, where)
     lead, kb, dev = _quantised(codes, scales, where)
     cols = _decoded_cols(cols, kb, where)
     n, nd = len(codes), len(lead) + 1
@@ -363,7 +369,7 @@ def vrc_mx4_matmul(a_codes, a_scales, b_codes, b_scales, recv=None, dtype=None, 
     where = "vrc_mx4_matmul"
     torch = _torch()
     dtype = torch.bfloat16 if dtype is None else dtype
-    code = _out_code(dtype, where)
+    code = _float_code(dtype, where)
     if join not in MX4_JOINS:
         raise ValueError(f"join must be one of {sorted(MX4_JOINS)}")
     lead, kb, dev = _quantised(a_codes, a_scales, where)
