@@ -182,23 +182,44 @@ struct ChunkArgs {
     uint64_t width[kMaxRanks];
     RowSplit g[kMaxRanks];
     FastDiv by_nvb[kMaxRanks];
-    uint64_t rows, stride;
-    uint64_t tiles;  // wave tiles per chunk (the largest chunk's)
-    uint64_t slots[kMaxRanks];  // scalar slots of each chunk
-    FastDiv by_tile;            // division of a tile's number, and of a vector's by by_nvb
+    uint64_t rows, stride, last_width;
+    uint64_t tiles;   // wave tiles per chunk (the largest chunk's)
+    FastDiv by_tile;  // division of a tile's number, and of a vector's by by_nvb
     int n;
-    bool small;    // those numbers are below 2^31
-    bool scalars;  // some chunk has slots
+    bool small;  // those numbers are below 2^31
+    // The elements that no vector holds: slots, numbered row by row and in a row chunk
+    // by chunk, so that neighbouring lanes have neighbouring elements of the whole
+    // tensor; chunk c's are from first_slot[c] of a row's row_slots.
+    uint64_t slots, row_slots;
+    uint32_t first_slot[kMaxRanks];
+    FastDiv by_row_slots, by_n;
+    bool small_slots;  // their numbers are below 2^31
+    // Narrow rows: no vectors, and slot k is elements 4k .. 4k + 3 of the whole tensor, one
+    // of the generator's blocks, in whatever chunks and rows they lie.
+    bool narrow;
+    uint64_t total;
+    FastDiv by_width;
     // Each row's vectors start at its first element whose index is a multiple of four
     // (else the chunk's split g puts them on the grid of its stores).  A vector off
     // the generator's blocks of four needs one block more: twice the work in fp32.
     bool on_blocks;
 };
 
-// Elements of a row before its vectors, on_blocks.
+// Chunk c's off and width without an array (the last of a flat split has the remainder).
+__device__ __forceinline__ uint64_t chunk_off(const ChunkArgs& a, int c) { return (uint64_t)c * a.width[0]; }
+__device__ __forceinline__ uint64_t chunk_width(const ChunkArgs& a, int c)
+{
+    return c == a.n - 1 ? a.last_width : a.width[0];
+}
+
+// Elements of a row before its vectors, on_blocks: at most three, and less than a vector
+// after them.
+template <class T>
+constexpr uint32_t kBlockSlots = T::VEC + 2;
+
 __device__ __forceinline__ uint64_t before_block(const ChunkArgs& a, int c, uint64_t row)
 {
-    return (0 - (a.off[c] + row * a.stride)) & 3;
+    return (0 - (chunk_off(a, c) + row * a.stride)) & 3;
 }
 
 // Wave tile t: chunk and tile within it.  A flat split (rows == 1) walks the
@@ -230,21 +251,137 @@ __device__ __forceinline__ bool vector_place(const ChunkArgs& a, int c, uint64_t
     return col + T::VEC <= a.width[c];
 }
 
-// Slot k's element of chunk c's scalars; false where it has none.
+// What a lane needs of a chunk that it found by its own element, copied into LDS: by a
+// lane's own index these would be vector loads of the kernel's arguments (4 x [262144,
+// 4 x 63] bf16 166 us, 235 us by such loads).
+struct ChunkTable {
+    const char* in[kMaxRanks];
+    char* out[kMaxRanks];
+    uint32_t head[kMaxRanks];
+    uint64_t body[kMaxRanks];  // elements in a row's vectors
+
+    __device__ __forceinline__ void put(int c, const char* from, char* to, const RowSplit& g, uint64_t vec)
+    {
+        in[c] = from;
+        out[c] = to;
+        head[c] = (uint32_t)g.head;
+        body[c] = g.nvb * vec;
+    }
+};
+
+// Slot k's chunk, row and column; false where it has no element.
 template <class T>
-__device__ __forceinline__ bool scalar_place(const ChunkArgs& a, int c, uint64_t k, uint64_t& row, uint64_t& col)
+__device__ __forceinline__ bool scalar_place(const ChunkArgs& a, const ChunkTable& table, uint64_t k, int& c, uint64_t& row,
+                                             uint64_t& col)
 {
+    row = a.small_slots ? a.by_row_slots.div((uint32_t)k) : k / a.row_slots;
+    uint32_t j = (uint32_t)(k - row * a.row_slots);
     if (!a.on_blocks) {
-        scalar_slot(k, a.g[c], T::VEC, row, col);
+        c = 0;
+        uint32_t first = 0;
+        for (int d = 1; d < a.n; d++) {
+            if (j < a.first_slot[d]) continue;
+            c = d;
+            first = a.first_slot[d];
+        }
+        j -= first;
+        col = j;
+        if (j >= table.head[c]) col += table.body[c];
         return true;
     }
-    constexpr uint64_t S = T::VEC + 2;
-    row = k / S;
-    const uint64_t j = k - row * S, head = before_block(a, c, row), width = a.width[c];
+    c = (int)(j / kBlockSlots<T>);
+    j -= (uint32_t)c * kBlockSlots<T>;
+    col = j;
+    const uint64_t head = before_block(a, c, row), width = chunk_width(a, c);
     const uint64_t vectors = width > head ? (width - head) / T::VEC : 0;
-    col = j < head ? j : vectors * T::VEC + j;
+    if (j >= head) col += vectors * T::VEC;
     return col < width;
 }
+
+// Narrow rows: where the elements 4k .. 4k + 3 of the whole tensor lie.
+struct NarrowPlace {
+    int c;
+    uint64_t row, col;
+
+    __device__ NarrowPlace(const ChunkArgs& a, uint64_t k)
+    {
+        const uint64_t q = a.small_slots ? a.by_width.div((uint32_t)k * 4) : 4 * k / a.width[0];
+        row = a.small_slots ? a.by_n.div((uint32_t)q) : q / (uint64_t)a.n;
+        c = (int)(q - row * (uint64_t)a.n);
+        col = 4 * k - q * a.width[0];
+    }
+    // In a chunk's own buffer.
+    __device__ uint64_t at(const ChunkArgs& a) const { return row * a.width[0] + col; }
+    // The four lie in one row of one chunk.
+    __device__ bool together(const ChunkArgs& a) const { return col + 4 <= a.width[0]; }
+    __device__ void next(const ChunkArgs& a)
+    {
+        if (++col < a.width[0]) return;
+        col = 0;
+        if (++c < a.n) return;
+        c = 0;
+        row++;
+    }
+};
+
+// Four consecutive elements as they are stored, at any element.
+template <class T>
+struct Quad {
+    typedef uint32_t Words __attribute__((ext_vector_type(T::ESZ), aligned(1)));
+    typename T::S s[4];
+
+    __device__ __forceinline__ void load(const char* p)
+    {
+        const Words v = __builtin_nontemporal_load((global_ptr<const Words>)p);
+#pragma unroll
+        for (int e = 0; e < 4; e++) s[e] = T::ESZ == 4 ? v[e % T::ESZ] : (typename T::S)(v[e / 2] >> (16 * (e & 1)));
+    }
+    __device__ __forceinline__ void store(char* p) const
+    {
+        Words v;
+#pragma unroll
+        for (int w = 0; w < T::ESZ; w++)
+            v[w] = T::ESZ == 4 ? (uint32_t)s[w] : (uint32_t)s[2 * w % 4] | (uint32_t)s[(2 * w + 1) % 4] << 16;
+        __builtin_nontemporal_store(v, (global_ptr<Words>)p);
+    }
+    // The first `left` of them; the others are zero.
+    __device__ __forceinline__ void load_part(const char* p, int left)
+    {
+#pragma unroll
+        for (int e = 0; e < 4; e++) s[e] = e < left ? load_s<T>(p + e * T::ESZ) : (typename T::S)0;
+    }
+    __device__ __forceinline__ void store_part(char* p, int left) const
+    {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (e < left) store_s<T>(p + e * T::ESZ, s[e]);
+    }
+    // From or to the chunks' own buffers.
+    __device__ __forceinline__ void gather(const ChunkArgs& a, const ChunkTable& t, NarrowPlace at, int left)
+    {
+        if (left == 4 && at.together(a)) {
+            load(t.in[at.c] + at.at(a) * T::ESZ);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            s[e] = e < left ? load_s<T>(t.in[at.c] + at.at(a) * T::ESZ) : (typename T::S)0;
+            at.next(a);
+        }
+    }
+    __device__ __forceinline__ void scatter(const ChunkArgs& a, const ChunkTable& t, NarrowPlace at, int left) const
+    {
+        if (left == 4 && at.together(a)) {
+            store(t.out[at.c] + at.at(a) * T::ESZ);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            if (e < left) store_s<T>(t.out[at.c] + at.at(a) * T::ESZ, s[e]);
+            at.next(a);
+        }
+    }
+};
 
 struct DropRsArgs {
     const char* src[kMaxRanks];
@@ -281,21 +418,75 @@ __global__ __launch_bounds__(64) void k_dropout_reduce_scatter(DropRsArgs a)
         for (int k = 0; k < T::VEC; k++) acc[k] = mask.apply(acc[k], bits, k);
         st16<true>(a.dst[c] + o, RES ? add_residual<T>(acc, res) : T::pack(acc));
     }
-    if (!ch.scalars) return;
-    for (int c = 0; c < N; c++) {
-        const uint64_t ns = ch.slots[c];
-        for (uint64_t k = blockIdx.x * W + lane; k < ns; k += (uint64_t)gridDim.x * W) {
-            uint64_t row, col;
-            if (!scalar_place<T>(ch, c, k, row, col)) continue;
-            const uint64_t i = ch.off[c] + row * ch.stride + col;
-            const uint64_t o = (row * ch.width[c] + col) * E;
-            float acc = T::widen(load_s<T>(a.src[0] + i * E));
+    if (ch.slots == 0) return;
+    __shared__ ChunkTable table;
+    if (lane == 0) {
 #pragma unroll
-            for (int r = 1; r < N; r++) acc += T::widen(load_s<T>(a.src[r] + i * E));
-            acc = mask.apply(acc, mask.keep<1>(i), 0);
-            if constexpr (RES) acc += T::widen(load_s<T>(a.res[c] + o));
-            store_s<T>(a.dst[c] + o, T::narrow(acc));
+        for (int c = 0; c < N; c++) table.put(c, a.res[c], a.dst[c], ch.g[c], T::VEC);
+    }
+    __syncthreads();
+    for (uint64_t k = blockIdx.x * W + lane; k < ch.slots; k += (uint64_t)gridDim.x * W) {
+        int c;
+        uint64_t row, col;
+        if (!scalar_place<T>(ch, table, k, c, row, col)) continue;
+        const uint64_t i = chunk_off(ch, c) + row * ch.stride + col;
+        const uint64_t o = (row * chunk_width(ch, c) + col) * E;
+        typename T::S in[N], res = 0;
+#pragma unroll
+        for (int r = 0; r < N; r++) in[r] = load_s<T>(a.src[r] + i * E);
+        if constexpr (RES) res = load_s<T>(table.in[c] + o);
+        issue_loads_first();
+        float acc = T::widen(in[0]);
+#pragma unroll
+        for (int r = 1; r < N; r++) acc += T::widen(in[r]);
+        acc = mask.apply(acc, mask.keep<1>(i), 0);
+        if constexpr (RES) acc += T::widen(res);
+        store_s<T>(table.out[c] + o, T::narrow(acc));
+    }
+}
+
+// Narrow rows: a lane folds four elements of the whole tensor's rows, which lie together
+// in every input, draws their one block of the mask, and writes them to the chunks that
+// they belong to.  8 x [16384, 8 x 7] fp16, a stream of 17 MB, 7.3 us; [131072, 8 x 32]
+// 0.6 GB, 130 us, 4.6 TB/s.
+template <class T, int N, bool RES>
+__global__ __launch_bounds__(64) void k_dropout_reduce_scatter_narrow(DropRsArgs a)
+{
+    constexpr uint64_t W = 64, E = T::ESZ;
+    const Mask mask(a.m);
+    const uint64_t lane = threadIdx.x;
+    const ChunkArgs& ch = a.ch;
+    __shared__ ChunkTable table;
+    if (lane == 0) {
+#pragma unroll
+        for (int c = 0; c < N; c++) table.put(c, a.res[c], a.dst[c], ch.g[c], 0);
+    }
+    __syncthreads();
+    for (uint64_t k = blockIdx.x * W + lane; k < ch.slots; k += (uint64_t)gridDim.x * W) {
+        const uint64_t i = 4 * k;
+        const int left = ch.total - i < 4 ? (int)(ch.total - i) : 4;
+        Quad<T> x[N], res = {};
+        if (left == 4) {
+#pragma unroll
+            for (int r = 0; r < N; r++) x[r].load(a.src[r] + i * E);
+        } else {
+#pragma unroll
+            for (int r = 0; r < N; r++) x[r].load_part(a.src[r] + i * E, left);
         }
+        const NarrowPlace to(ch, k);
+        if constexpr (RES) res.gather(ch, table, to, left);
+        issue_loads_first();
+        const uint32_t bits = mask.keep<4>(i);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            float acc = T::widen(x[0].s[e]);
+#pragma unroll
+            for (int r = 1; r < N; r++) acc += T::widen(x[r].s[e]);
+            acc = mask.apply(acc, bits, e);
+            if constexpr (RES) acc += T::widen(res.s[e]);
+            x[0].s[e] = T::narrow(acc);
+        }
+        x[0].scatter(ch, table, to, left);
     }
 }
 
@@ -329,16 +520,45 @@ __global__ __launch_bounds__(64) void k_dropout_all_gather(DropAgArgs a)
         const u32x4 out = T::pack(x);
         for (int r = 0; r < ch.n; r++) st16<true>(a.dst[r] + i * E, out);
     }
-    if (!ch.scalars) return;
-    for (int c = 0; c < ch.n; c++) {
-        const uint64_t ns = ch.slots[c];
-        for (uint64_t k = blockIdx.x * W + lane; k < ns; k += (uint64_t)gridDim.x * W) {
-            uint64_t row, col;
-            if (!scalar_place<T>(ch, c, k, row, col)) continue;
-            const uint64_t i = ch.off[c] + row * ch.stride + col;
-            const float x = T::widen(load_s<T>(a.src[c] + (row * ch.width[c] + col) * E));
-            const typename T::S s = T::narrow(mask.apply(x, mask.keep<1>(i), 0));
-            for (int r = 0; r < ch.n; r++) store_s<T>(a.dst[r] + i * E, s);
+    if (ch.slots == 0) return;
+    __shared__ ChunkTable table;
+    if (lane < (uint64_t)ch.n) table.put((int)lane, a.src[lane], nullptr, ch.g[lane], T::VEC);
+    __syncthreads();
+    for (uint64_t k = blockIdx.x * W + lane; k < ch.slots; k += (uint64_t)gridDim.x * W) {
+        int c;
+        uint64_t row, col;
+        if (!scalar_place<T>(ch, table, k, c, row, col)) continue;
+        const uint64_t i = chunk_off(ch, c) + row * ch.stride + col;
+        const float x = T::widen(load_s<T>(table.in[c] + (row * chunk_width(ch, c) + col) * E));
+        const typename T::S s = T::narrow(mask.apply(x, mask.keep<1>(i), 0));
+        for (int r = 0; r < ch.n; r++) store_s<T>(a.dst[r] + i * E, s);
+    }
+}
+
+// Narrow rows: a lane gathers four elements of the outputs' rows.  8 x [16384, 7] fp16
+// 7.7 us; [131072, 56] 1.06 GB, 260 us, 4.1 TB/s (830 us by vectors and single elements).
+template <class T>
+__global__ __launch_bounds__(64) void k_dropout_all_gather_narrow(DropAgArgs a)
+{
+    constexpr uint64_t W = 64, E = T::ESZ;
+    const Mask mask(a.m);
+    const uint64_t lane = threadIdx.x;
+    const ChunkArgs& ch = a.ch;
+    __shared__ ChunkTable table;
+    if (lane < (uint64_t)ch.n) table.put((int)lane, a.src[lane], nullptr, ch.g[lane], 0);
+    __syncthreads();
+    for (uint64_t k = blockIdx.x * W + lane; k < ch.slots; k += (uint64_t)gridDim.x * W) {
+        const uint64_t i = 4 * k;
+        const int left = ch.total - i < 4 ? (int)(ch.total - i) : 4;
+        Quad<T> x;
+        x.gather(ch, table, NarrowPlace(ch, k), left);
+        const uint32_t bits = mask.keep<4>(i);
+#pragma unroll
+        for (int e = 0; e < 4; e++) x.s[e] = T::narrow(mask.apply(T::widen(x.s[e]), bits, e));
+        if (left == 4) {
+            for (int r = 0; r < ch.n; r++) x.store(a.dst[r] + i * E);
+        } else {
+            for (int r = 0; r < ch.n; r++) x.store_part(a.dst[r] + i * E, left);
         }
     }
 }
@@ -348,8 +568,7 @@ __global__ __launch_bounds__(64) void k_dropout_all_gather(DropAgArgs a)
 // ---------------------------------------------------------------------------
 using namespace host;
 
-// Workgroups: one per wave tile, up to `per_cu` per CU; tails and heads need
-// at least one.
+// Workgroups: one per wave tile, up to `per_cu` per CU, and at least one.
 unsigned wave_grid(uint64_t tiles, int cus, int per_cu)
 {
     const uint64_t cap = (uint64_t)cus * (uint64_t)per_cu;
@@ -384,6 +603,16 @@ int reduce_scatter_waves(int loads, uint64_t bytes)
 // CU (one rank 4.6 TB/s, 16 waves 4.2; 8 ranks 4.8 with 8 to 64, and 1 store in
 // flight per wave 4.4-4.8).
 constexpr int kGatherWaves = 64;
+
+// The workgroups of a call on chunks.  Where more elements go one by one than in
+// vectors, its time is theirs: a wave for every 64 of them, up to kScalarWaves per CU.
+constexpr int kScalarWaves = 32;
+
+unsigned chunk_grid(const ChunkArgs& a, int cus, int per_cu)
+{
+    const uint64_t tiles = a.tiles * (uint64_t)a.n, by_slots = (a.slots + 63) / 64;
+    return by_slots > tiles ? wave_grid(by_slots, cus, per_cu > kScalarWaves ? per_cu : kScalarWaves) : wave_grid(tiles, cus, per_cu);
+}
 
 template <class T, int N, int RES>
 vrc_status_t launch_ar(const DropArArgs& a, int cus, hipStream_t st)
@@ -433,15 +662,29 @@ vrc_status_t allreduce_typed(const char* const* x, const char* const* res, char*
     return VRC_ERR_INVALID_ARG;
 }
 
+// Narrow rows, of `bytes` in a rank's part.  A row's first and last elements go one by
+// one where they are no whole vectors, and rows of a few vectors lie on as many memory
+// lines as whole lines would.  us by vectors / by blocks of four of the whole tensor, on
+// 8 ranks of 16384 rows: fp16 reduce-scatter of 9 elements 31 / 8, 23 44 / 17, 47 61 / 36,
+// fp32 of 16 27 / 13; of 8192 rows fp16: of 56 22 / 16, but 64 17 / 18 and, with
+// residuals, 120 39 / 41.  2 ranks of 524288 rows, bf16: 8 16.4 / 14.8, 48 87 / 88.
+constexpr bool narrow_rs(uint64_t bytes) { return bytes < 128; }
+
+// The all-gather, 8192 rows on 8 ranks, fp16: 100 elements 45 / 33, 136 55 / 42, 200
+// 71 / 60, 257 110 / 79, but whole lines 64 18 / 19, 128 31 / 35; 2 ranks of 65536 rows,
+// bf16: 136 45 / 29, 257 64 / 63, whole lines 256 41 / 43.
+constexpr bool narrow_ag(uint64_t bytes) { return bytes < 512 && bytes % 128 != 0; }
+
 // The chunks of a tensor of `total` elements split over n ranks: flat for
 // outer == 1, by columns otherwise.  `ref` gives the address that chunk c's
 // vector grid follows, unless `blocks` and the generator's blocks of four lie
 // otherwise.
 template <class T, class Ref>
-ChunkArgs make_chunks(int n, uint64_t total, uint64_t outer, bool blocks, Ref ref)
+ChunkArgs make_chunks(int n, uint64_t total, uint64_t outer, bool blocks, bool narrow, Ref ref)
 {
     ChunkArgs a = {};
     a.n = n;
+    if (n == 1) outer = 1;  // one chunk is the tensor
     a.rows = outer;
     a.stride = total / outer;
     for (int c = 0; c < n; c++) {
@@ -453,18 +696,44 @@ ChunkArgs make_chunks(int n, uint64_t total, uint64_t outer, bool blocks, Ref re
         }
         a.on_blocks = a.on_blocks || (blocks && ((outer > 1 && a.stride % 4 != 0) || a.off[c] % 4 != 0));
     }
+    a.total = total;
+    a.last_width = a.width[n - 1];
+    a.narrow = narrow && outer > 1;
+    a.by_n = FastDiv::of((uint64_t)n);
+    if (a.narrow) {
+        a.slots = (total + 3) / 4;
+        a.small_slots = total < 1ull << 31;
+        a.by_width = FastDiv::of(a.width[0]);
+        return a;
+    }
     for (int c = 0; c < n; c++) {
         a.g[c] = a.on_blocks ? RowSplit{0, a.width[c] / T::VEC, 0} : split_rows(ref(c, a.off[c]), a.width[c], T::ESZ);
         a.by_nvb[c] = FastDiv::of(a.g[c].nvb);
         const uint64_t tiles = (a.rows * a.g[c].nvb + 63) / 64;
         if (tiles > a.tiles) a.tiles = tiles;
-        a.slots[c] = a.rows * (a.on_blocks ? T::VEC + 2 : a.g[c].head + a.g[c].tail);
-        a.scalars = a.scalars || a.slots[c];
+        a.first_slot[c] = (uint32_t)a.row_slots;
+        a.row_slots += a.on_blocks ? kBlockSlots<T> : a.g[c].head + a.g[c].tail;
     }
+    a.slots = a.rows * a.row_slots;
+    a.by_row_slots = FastDiv::of(a.row_slots);
+    a.small_slots = a.slots < 1ull << 31;
     // a chunk's vectors are at most 64 of each of its tiles
     a.small = a.tiles * 64 < 1ull << 31 && a.tiles * (uint64_t)n < 1ull << 31;
     a.by_tile = FastDiv::of(outer == 1 ? a.tiles : (uint64_t)n);
     return a;
+}
+
+template <class T, int N, bool RES>
+vrc_status_t launch_rs(const DropRsArgs& a, unsigned grid, hipStream_t st)
+{
+    if constexpr (N > 1) {
+        if (a.ch.narrow) {
+            k_dropout_reduce_scatter_narrow<T, N, RES><<<grid, 64, 0, st>>>(a);
+            return check_launch();
+        }
+    }
+    k_dropout_reduce_scatter<T, N, RES><<<grid, 64, 0, st>>>(a);
+    return check_launch();
 }
 
 template <class T>
@@ -477,15 +746,12 @@ vrc_status_t reduce_scatter_typed(const char* const* x, const char* const* res, 
         a.dst[r] = y[r];
         a.res[r] = res ? res[r] : nullptr;
     }
-    a.ch = make_chunks<T>(n, count, outer, true, [&](int c, uint64_t) { return (uintptr_t)y[c]; });
+    a.ch = make_chunks<T>(n, count, outer, true, narrow_rs(count / outer / (uint64_t)n * T::ESZ), [&](int c, uint64_t) { return (uintptr_t)y[c]; });
     a.m = m;
-    const unsigned grid = wave_grid(a.ch.tiles * (uint64_t)n, cus, reduce_scatter_waves(n + (res ? 1 : 0), n * count * T::ESZ));
+    const unsigned grid = chunk_grid(a.ch, cus, reduce_scatter_waves(n + (res ? 1 : 0), n * count * T::ESZ));
     switch (n) {
-#define VRC_CASE(N)                                                                  \
-    case N:                                                                          \
-        if (res) k_dropout_reduce_scatter<T, N, true><<<grid, 64, 0, st>>>(a);       \
-        else k_dropout_reduce_scatter<T, N, false><<<grid, 64, 0, st>>>(a);          \
-        return check_launch();
+#define VRC_CASE(N) \
+    case N: return res ? launch_rs<T, N, true>(a, grid, st) : launch_rs<T, N, false>(a, grid, st);
         VRC_CASE(1)
         VRC_FOR_N(VRC_CASE)
 #undef VRC_CASE
@@ -505,9 +771,11 @@ vrc_status_t all_gather_typed(const char* const* x, char* const* y, int n, uint6
         dst[r] = (uintptr_t)y[r];
     }
     const uintptr_t at = write_ref(dst, n);
-    a.ch = make_chunks<T>(n, total, outer, outer > 1, [&](int, uint64_t off) { return at + off * T::ESZ; });
+    a.ch = make_chunks<T>(n, total, outer, outer > 1, narrow_ag(total / outer / (uint64_t)n * T::ESZ), [&](int, uint64_t off) { return at + off * T::ESZ; });
     a.m = m;
-    k_dropout_all_gather<T><<<wave_grid(a.ch.tiles * (uint64_t)n, cus, kGatherWaves), 64, 0, st>>>(a);
+    const unsigned grid = chunk_grid(a.ch, cus, kGatherWaves);
+    if (a.ch.narrow) k_dropout_all_gather_narrow<T><<<grid, 64, 0, st>>>(a);
+    else k_dropout_all_gather<T><<<grid, 64, 0, st>>>(a);
     return check_launch();
 }
 
