@@ -81,10 +81,14 @@ struct Mask {
         return bits >> ph;
     }
 
-    // mask * scale * a, with +0 for a dropped element.
+    // mask * scale * a, with +0 for a dropped element.  The product is an fp32 value of
+    // its own: seeing what becomes of it, the compiler would join it with a conversion to
+    // fp16 in one operation, which rounds once and makes -0 a +0.
     __device__ __forceinline__ float apply(float a, uint32_t bits, int j) const
     {
-        return (bits >> j & 1u) ? a * scale : 0.0f;
+        float y = a * scale;
+        __asm__("" : "+v"(y));
+        return (bits >> j & 1u) ? y : 0.0f;
     }
 };
 
