@@ -9,6 +9,8 @@
 // multiplications (20 of 32 x 32 bits for four elements) run beside them.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "vrc_ops_host.hpp"
 
 namespace vrc {
@@ -83,11 +85,13 @@ struct Mask {
 
     // mask * scale * a, with +0 for a dropped element.  The product is an fp32 value of
     // its own: seeing what becomes of it, the compiler would join it with a conversion to
-    // fp16 in one operation, which rounds once and makes -0 a +0.
+    // fp16 in one operation, which rounds once and makes -0 a +0.  (It has no such
+    // operation for the other types.)
+    template <class T>
     __device__ __forceinline__ float apply(float a, uint32_t bits, int j) const
     {
         float y = a * scale;
-        __asm__("" : "+v"(y));
+        if constexpr (std::is_same<T, F16>::value) __asm__("" : "+v"(y));
         return (bits >> j & 1u) ? y : 0.0f;
     }
 };
@@ -150,7 +154,7 @@ __global__ __launch_bounds__(64) void k_dropout_allreduce(DropArArgs a)
         fold_f32<T, N>(in, acc);
         const uint32_t bits = mask.keep<T::VEC>(a.g.head + v * T::VEC);
 #pragma unroll
-        for (int i = 0; i < T::VEC; i++) acc[i] = mask.apply(acc[i], bits, i);
+        for (int i = 0; i < T::VEC; i++) acc[i] = mask.apply<T>(acc[i], bits, i);
         u32x4 out = RES == 0 ? T::pack(acc) : u32x4{};
         if constexpr (RES == 1) out = add_residual<T>(acc, res[0]);
 #pragma unroll
@@ -166,7 +170,7 @@ __global__ __launch_bounds__(64) void k_dropout_allreduce(DropArArgs a)
         float acc = T::widen(load_s<T>(a.src[0] + i * E));
 #pragma unroll
         for (int r = 1; r < N; r++) acc += T::widen(load_s<T>(a.src[r] + i * E));
-        acc = mask.apply(acc, mask.keep<1>(i), 0);
+        acc = mask.apply<T>(acc, mask.keep<1>(i), 0);
         float x[NR ? NR : 1];
 #pragma unroll
         for (int r = 0; r < NR; r++) x[r] = T::widen(load_s<T>(a.res[r] + i * E));
@@ -419,7 +423,7 @@ __global__ __launch_bounds__(64) void k_dropout_reduce_scatter(DropRsArgs a)
         fold_f32<T, N>(in, acc);
         const uint32_t bits = mask.keep<T::VEC>(i);
 #pragma unroll
-        for (int k = 0; k < T::VEC; k++) acc[k] = mask.apply(acc[k], bits, k);
+        for (int k = 0; k < T::VEC; k++) acc[k] = mask.apply<T>(acc[k], bits, k);
         st16<true>(a.dst[c] + o, RES ? add_residual<T>(acc, res) : T::pack(acc));
     }
     if (ch.slots == 0) return;
@@ -443,7 +447,7 @@ __global__ __launch_bounds__(64) void k_dropout_reduce_scatter(DropRsArgs a)
         float acc = T::widen(in[0]);
 #pragma unroll
         for (int r = 1; r < N; r++) acc += T::widen(in[r]);
-        acc = mask.apply(acc, mask.keep<1>(i), 0);
+        acc = mask.apply<T>(acc, mask.keep<1>(i), 0);
         if constexpr (RES) acc += T::widen(res);
         store_s<T>(table.out[c] + o, T::narrow(acc));
     }
@@ -486,7 +490,7 @@ __global__ __launch_bounds__(64) void k_dropout_reduce_scatter_narrow(DropRsArgs
             float acc = T::widen(x[0].s[e]);
 #pragma unroll
             for (int r = 1; r < N; r++) acc += T::widen(x[r].s[e]);
-            acc = mask.apply(acc, bits, e);
+            acc = mask.apply<T>(acc, bits, e);
             if constexpr (RES) acc += T::widen(res.s[e]);
             x[0].s[e] = T::narrow(acc);
         }
@@ -520,7 +524,7 @@ __global__ __launch_bounds__(64) void k_dropout_all_gather(DropAgArgs a)
         float x[T::VEC];
         T::unpack(in, x);
 #pragma unroll
-        for (int k = 0; k < T::VEC; k++) x[k] = mask.apply(x[k], bits, k);
+        for (int k = 0; k < T::VEC; k++) x[k] = mask.apply<T>(x[k], bits, k);
         const u32x4 out = T::pack(x);
         for (int r = 0; r < ch.n; r++) st16<true>(a.dst[r] + i * E, out);
     }
@@ -534,7 +538,7 @@ __global__ __launch_bounds__(64) void k_dropout_all_gather(DropAgArgs a)
         if (!scalar_place<T>(ch, table, k, c, row, col)) continue;
         const uint64_t i = chunk_off(ch, c) + row * ch.stride + col;
         const float x = T::widen(load_s<T>(table.in[c] + (row * chunk_width(ch, c) + col) * E));
-        const typename T::S s = T::narrow(mask.apply(x, mask.keep<1>(i), 0));
+        const typename T::S s = T::narrow(mask.apply<T>(x, mask.keep<1>(i), 0));
         for (int r = 0; r < ch.n; r++) store_s<T>(a.dst[r] + i * E, s);
     }
 }
@@ -558,7 +562,7 @@ __global__ __launch_bounds__(64) void k_dropout_all_gather_narrow(DropAgArgs a)
         x.gather(ch, table, NarrowPlace(ch, k), left);
         const uint32_t bits = mask.keep<4>(i);
 #pragma unroll
-        for (int e = 0; e < 4; e++) x.s[e] = T::narrow(mask.apply(T::widen(x.s[e]), bits, e));
+        for (int e = 0; e < 4; e++) x.s[e] = T::narrow(mask.apply<T>(T::widen(x.s[e]), bits, e));
         if (left == 4) {
             for (int r = 0; r < ch.n; r++) x.store(a.dst[r] + i * E);
         } else {
