@@ -81,23 +81,14 @@ def _pointers(tensors):
     return _POINTERS[len(tensors)](*[t.data_ptr() for t in tensors])
 
 
-# New outputs of one shape are parts of one allocation while each holds at most
-# this many bytes, in whole vectors: eight allocations cost 14 us of host time, one
-# with its parts 5 us, which is what a small call takes; larger calls hide it, and
-# keep tensors that can be freed one by one.  To autograd the parts are separate
-# tensors, not views of one: writing one in place leaves the others' versions alone.
-SHARED_ALLOCATION_BYTES = 4 << 20
-
-
 def _allocate(shapes, dtype, device):
+    """New outputs, each with a storage of its own: parts of one allocation would take
+    half the host time (5 us for eight instead of 10), but one that grows in place
+    would grow over the others, and keeping or saving one would keep or write them all."""
     torch = _torch()
-    first, n = shapes[0], len(shapes)
-    size = _prod(first) * dtype.itemsize
-    if n > 1 and first and 0 < size <= SHARED_ALLOCATION_BYTES and size % 16 == 0 and shapes.count(first) == n:
-        return list(torch.empty((n * first[0], *first[1:]), dtype=dtype, device=device).unsafe_split(first[0]))
+    first, like = shapes[0], torch.empty_like
     t0 = torch.empty(first, dtype=dtype, device=device)
-    return [t0] + [torch.empty_like(t0) if s == first else torch.empty(s, dtype=dtype, device=device)
-                   for s in shapes[1:]]
+    return [t0] + [like(t0) if s == first else torch.empty(s, dtype=dtype, device=device) for s in shapes[1:]]
 
 
 def _outputs(recv, shapes, like, where, stream, dtype=None):
