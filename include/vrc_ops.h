@@ -57,7 +57,8 @@ typedef struct {
     unsigned long long offset; /* the counter's upper half: one value per mask */
     /* NULL, or a DEVICE address (8-byte aligned) of a number that is added to
      * `offset` (modulo 2^64) when the kernel runs: a captured graph draws a new
-     * mask at every replay once the caller advances it. */
+     * mask at every replay once the caller advances it.  It lies in no output
+     * (VRC_ERR_ALIAS). */
     const unsigned long long* offset_dev;
 } vrc_dropout_t;
 

@@ -73,6 +73,13 @@ int bufs(const char* const* p, int n, uint64_t bytes, Buf* out, int at)
     return at;
 }
 
+// The mask's offset in device memory among the inputs: no output may hold it.
+int offset_buf(const MaskArgs& m, Buf* in, int at)
+{
+    in[at] = {(uintptr_t)m.offset_dev, m.offset_dev ? sizeof(uint64_t) : 0};
+    return at + 1;
+}
+
 vrc_status_t allreduce_dropout_impl(const void* const* send, const void* const* residual, void* const* recv, int n,
                                     uint64_t count, int dtype, const vrc_dropout_t* d, hipStream_t st)
 {
@@ -88,11 +95,13 @@ vrc_status_t allreduce_dropout_impl(const void* const* send, const void* const* 
         return VRC_ERR_INVALID_ARG;
     const vrc_dtype_t dt = static_cast<vrc_dtype_t>(dtype);
     const uint64_t bytes = count * (uint64_t)esize(dt);
-    Buf in[2 * kMaxRanks], out[kMaxRanks];
+    Buf in[2 * kMaxRanks + 1], out[kMaxRanks];
     int ni = bufs(x, n, bytes, in, 0);
     if (residual) ni = bufs(res, n, bytes, in, ni);
+    const int operands = ni;
+    ni = offset_buf(m, in, ni);
     bufs(y, n, bytes, out, 0);
-    rc = check_outputs(out, n, in, ni, [n](int i, int j) { return i == j % n; });
+    rc = check_outputs(out, n, in, ni, [n, operands](int i, int j) { return j < operands && i == j % n; });
     if (rc) return rc;
     int cus;
     rc = begin_launch(&cus);
@@ -143,13 +152,15 @@ vrc_status_t reduce_scatter_dropout_impl(const void* const* send, const void* co
     char* y[kMaxRanks];
     if (!pointers(send, n, x) || !chunk_pointers(recv, n, cb, y) || (residual && !chunk_pointers(residual, n, cb, res)))
         return VRC_ERR_INVALID_ARG;
-    Buf in[2 * kMaxRanks], out[kMaxRanks];
+    Buf in[2 * kMaxRanks + 1], out[kMaxRanks];
     int ni = bufs(x, n, count * (uint64_t)esize(dt), in, 0);
     for (int c = 0; c < n; c++) {
         if (residual) in[ni++] = {(uintptr_t)res[c], cb[c]};
         out[c] = {(uintptr_t)y[c], cb[c]};
     }
-    rc = check_outputs(out, n, in, ni, [n](int i, int j) { return j == n + i; });
+    const int operands = ni;
+    ni = offset_buf(m, in, ni);
+    rc = check_outputs(out, n, in, ni, [n, operands](int i, int j) { return j < operands && j == n + i; });
     if (rc) return rc;
     int cus;
     rc = begin_launch(&cus);
@@ -173,10 +184,11 @@ vrc_status_t all_gather_dropout_impl(const void* const* send, void* const* recv,
     const char* x[kMaxRanks];
     char* y[kMaxRanks];
     if (!chunk_pointers(send, n, cb, x) || !pointers(recv, n, y)) return VRC_ERR_INVALID_ARG;
-    Buf in[kMaxRanks], out[kMaxRanks];
+    Buf in[kMaxRanks + 1], out[kMaxRanks];
     for (int c = 0; c < n; c++) in[c] = {(uintptr_t)x[c], cb[c]};
+    const int ni = offset_buf(m, in, n);
     bufs(y, n, total * (uint64_t)esize(dt), out, 0);
-    rc = check_outputs(out, n, in, n, [](int, int) { return false; });
+    rc = check_outputs(out, n, in, ni, [](int, int) { return false; });
     if (rc) return rc;
     int cus;
     rc = begin_launch(&cus);
