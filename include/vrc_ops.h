@@ -98,7 +98,8 @@ vrc_status_t vrc_reduce_scatter_dropout(const void* const* send, const void* con
  * tensor, which has `total` elements in `outer` rows.  With outer == 1 input c holds
  * its chunk c (vrc_chunk_range: the last chunk takes what the ranks do not divide);
  * with outer > 1 it holds [outer, total / outer / nranks].  For each element it is
- * one multiplication of an input, rounded once.  Outputs overlap no other buffer.
+ * one multiplication of an input in fp32, rounded to the type.  Outputs overlap no
+ * other buffer.
  * Gradient: each send[c]'s is vrc_reduce_scatter_dropout of the outputs'
  * gradients (same dropout, no residual).
  */
@@ -122,8 +123,10 @@ vrc_status_t vrc_mx4_quantize(const void* const* x, void* const* codes, void* co
 
 /*
  * Decode rank r's [rows, cols] matrix (codes laid out by VRC_MX4_ALONG_COLS)
- * into recv[r], for every rank.  Values are exact in fp32; fp16 and bf16 round
- * them to nearest even (overflow to infinity).
+ * into recv[r], for every rank.  Values are exact in fp32, but for magnitudes of
+ * 2^128 and more (scale byte 253 with 4 or 6, 254 with 2 to 6; the quantiser
+ * makes neither), which are infinite; fp16 and bf16 round to nearest even
+ * (overflow to infinity).
  */
 vrc_status_t vrc_mx4_dequantize(const void* const* codes, const void* const* scales, void* const* recv, int nranks,
                                 size_t rows, size_t cols, vrc_dtype_t dtype, vrc_stream_t stream);
@@ -149,7 +152,9 @@ typedef enum {
  * quantiser leaves them); recv[r]: [m, n] row-major, of type `dtype`.
  *   Each product of two codes is exact; sums are held in fp32 over all of k and,
  *   for VRC_MX4_SUM, over all ranks, and rounded once.  The order of the sum is
- *   fixed by the sizes, so equal calls give equal bits.
+ *   fixed by the sizes and by the device's number of CUs, so equal calls on one
+ *   device give equal bits.  A partial sum beyond fp32's range leaves its result
+ *   undefined.
  *   kblocks == 0 gives zeros.  Outputs overlap no other buffer.
  *   m, n < 2^31, kblocks < 2^20.
  * Gradients of recv = A B^T, with G the output's gradient: A's is G B, the product of

@@ -15,7 +15,7 @@
 namespace vrc {
 namespace host {
 thread_local int g_last_hip_error = 0;
-thread_local Plan* g_plan = nullptr;
+thread_local Plan* g_plan = nullptr;  // vrc_launch.hpp's launches look for one; this library records no plans
 }  // namespace host
 }  // namespace vrc
 
@@ -241,7 +241,8 @@ vrc_status_t mx4_quantize_impl(const void* const* x_, void* const* codes_, void*
     return run_mx4_quantize(x, codes, scales, n, rows, cols, dt, along_rows, cus, st);
 }
 
-// n_out: 0 for each rank's own matrix.
+// gather: every rank's matrix goes to every output, along the columns if by_cols; else
+// each to its own.
 vrc_status_t mx4_decode_impl(const void* const* codes_, const void* const* scales_, void* const* recv, int n, bool gather,
                              uint64_t rows, uint64_t cols, bool by_cols, int dtype, hipStream_t st)
 {

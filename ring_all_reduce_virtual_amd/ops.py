@@ -4,7 +4,9 @@ over virtual ranks (``libvrc_ops.so``).
 Like the collectives' functions these take one tensor per rank, check shapes
 and marshal pointers and the current HIP stream; the computation runs in HIP
 kernels.  Where a ``stream`` is given, outputs that the call allocates belong
-to that stream's pool."""
+to that stream's pool.  As with the collectives, autograd records none of the
+calls: outputs require no gradients, and each call's docstring names the calls
+that compute its gradients."""
 from __future__ import annotations
 
 import ctypes as C
