@@ -344,8 +344,11 @@ __global__ __launch_bounds__(256) void k_mx4_quantize_t(QuantTArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// Decoding.  A lane has eight codes (4 bytes in, 16 or 32 out), written to every
-// output.  blockIdx.y is the rank whose codes are read.
+// Decoding.  A lane has one vector of the output's type (eight codes, or four for
+// fp32), written to every output: a wave's stores fill whole lines.  (With eight codes
+// a lane in fp32 too, 32 bytes in two stores, each wrote half of every line: gather of
+// 8 x [20480, 128] 300 us, and 540 us where the halves were kept apart by THROTTLE.)
+// blockIdx.y is the rank whose codes are read.
 // FLAT: cols is a multiple of 32 and rows are packed in the outputs.  THROTTLE: a
 // wave waits for each store before the next, which keeps the outputs' streams from
 // crowding one another out.
@@ -359,22 +362,17 @@ struct DecodeArgs {
     FastDiv by_kb;
 };
 
+// One vector of a type from its codes.
 template <class T>
-__device__ __forceinline__ void decode8(uint32_t c, float s, uint32_t* w)
+__device__ __forceinline__ u32x4 decode_vec(uint32_t c, float s)
 {
     if constexpr (T::ESZ == 4) {
         const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
         const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
-        const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
-        const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
-        const float v[8] = {a.x, a.y, b.x, b.y, d.x, d.y, e.x, e.y};
-#pragma unroll
-        for (int i = 0; i < 8; i++) w[i] = __float_as_uint(v[i]);
+        return u32x4{__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)};
     } else {
-        w[0] = Mx4<T>::template decode<0>(c, s);
-        w[1] = Mx4<T>::template decode<1>(c, s);
-        w[2] = Mx4<T>::template decode<2>(c, s);
-        w[3] = Mx4<T>::template decode<3>(c, s);
+        return u32x4{Mx4<T>::template decode<0>(c, s), Mx4<T>::template decode<1>(c, s), Mx4<T>::template decode<2>(c, s),
+                     Mx4<T>::template decode<3>(c, s)};
     }
 }
 
@@ -382,38 +380,37 @@ template <class T, bool FLAT, bool THROTTLE>
 __global__ __launch_bounds__(256) void k_mx4_decode(DecodeArgs a)
 {
     constexpr uint64_t E = T::ESZ;
-    constexpr int D = T::ESZ * 2;
+    constexpr int V = T::VEC, LG = V == 8 ? 2 : 3;  // 2^LG vectors of a block
+    typedef typename std::conditional<V == 8, uint32_t, uint16_t>::type Codes;
     const int q = blockIdx.y;
-    const auto codes = (global_ptr<const uint32_t>)a.codes[q];
+    const auto codes = (global_ptr<const Codes>)a.codes[q];
     const auto scales = (global_ptr<const uint8_t>)a.scales[q];
     const int r0 = a.n_out ? 0 : q, r1 = a.n_out ? a.n_out : q + 1;
     const uint64_t step = (uint64_t)gridDim.x * 256;
     for (uint64_t g = (uint64_t)blockIdx.x * 256 + threadIdx.x; g < a.groups; g += step) {
-        uint32_t w[D];
-        decode8<T>(codes[g], scale_float(scales[g >> 2]), w);
+        const u32x4 x = decode_vec<T>(codes[g], scale_float(scales[g >> LG]));
         uint64_t at = (uint64_t)q * a.slab;
-        int64_t left = 8;
+        int64_t left = V;
         if constexpr (FLAT) {
-            at += g * 8;
+            at += g * V;
         } else {
-            const uint64_t b = g >> 2;
-            const uint64_t row = (a.groups >> 33) ? b / a.kb : a.by_kb.div((uint32_t)b);
-            const uint64_t col = (b - row * a.kb) * 32 + (g & 3) * 8;
+            const uint64_t b = g >> LG;
+            const uint64_t row = (a.groups >> (31 + LG)) ? b / a.kb : a.by_kb.div((uint32_t)b);
+            const uint64_t col = (b - row * a.kb) * 32 + (g & ((1 << LG) - 1)) * V;
             left = (int64_t)a.cols - (int64_t)col;
             at += row * a.stride + col;
         }
-        if (left >= 8) {
-            for (int r = r0; r < r1; r++)
-#pragma unroll
-                for (int i = 0; i < D / 4; i++) {
-                    st16<true>(a.dst[r] + at * E + 16 * i, u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]});
-                    if constexpr (THROTTLE) wait_vmem_below<0>();
-                }
+        if (left >= V) {
+            for (int r = r0; r < r1; r++) {
+                st16<true>(a.dst[r] + at * E, x);
+                if constexpr (THROTTLE) wait_vmem_below<0>();
+            }
         } else {
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
+            for (int i = 0; i < V; i++) {
                 if (i >= left) continue;
-                const uint32_t s = E == 4 ? w[i % D] : w[(i / 2) % D] >> (16 * (i & 1));
+                const uint32_t s = E == 4 ? w[i % 4] : w[i / 2 % 4] >> (16 * (i & 1));
                 for (int r = r0; r < r1; r++) store_s<T>(a.dst[r] + (at + i) * E, (typename T::S)s);
             }
         }
@@ -490,12 +487,16 @@ vrc_status_t decode_typed(const char* const* codes, const char* const* scales, c
     a.n_out = n_out;
     a.cols = cols;
     a.kb = (cols + 31) / 32;
-    a.groups = rows * a.kb * 4;
+    a.groups = rows * a.kb * (32 / T::VEC);
     a.slab = slab;
     a.stride = stride;
     a.by_kb = FastDiv::of(a.kb);
-    // A gather keeps one store in flight per wave, 16 workgroups per CU: 8 x [20480,
-    // 128] fp16 60 us, against 67-70 us with its stores back to back at 8 to 64 per CU.
+    // A gather keeps one store in flight per wave, 16 workgroups per CU: us with / without
+    // that wait, along the rows 8 x [8192, 4096] bf16 773 / 893, [20480, 128] fp16 61 / 66,
+    // fp32 119 / 127, 2 x [65536, 512] fp32 92 / 97, 4 x [4096, 4096] fp16 103 / 98, 16 x
+    // [4096, 1024] bf16 389 / 383; along the columns within 3 % either way (8 x [8192, 4096]
+    // 799 / 794); 8 x [1, 4096] 4.8 / 4.2.  64 workgroups per CU come to the same, but for
+    // rows of odd lengths (8 x [5003, 1001] fp16 170, by 64 154).
     const dim3 grid(block_grid(a.groups, 256, n, cus, n_out > 1 ? 16 : 32), (unsigned)n);
     const bool flat = cols % 32 == 0 && stride == cols;
     if (n_out > 1) {

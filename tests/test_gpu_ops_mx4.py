@@ -6,6 +6,7 @@ import torch
 
 from tests import ops_reference as ref
 from tests.test_gpu_ops import DEV, DT, check_product, check_quantised, product, random_mx4, say, vrc  # noqa: F401
+from tests.test_gpu_ops_narrow import replay_us
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +92,18 @@ def test_decode_past_fp32(vrc):  # noqa: F811
                 assert torch.isinf(got[i]) and torch.signbit(got[i]) == (i % 16 >= 8), (byte, i)
             else:
                 assert got[i] == want[i], (byte, i)
+
+
+@pytest.mark.parametrize("dim", [0, -1])
+def test_gather_in_fp32_takes_its_bytes_time(vrc, dim):  # noqa: F811
+    """Twice the bytes of a 16-bit gather, and little more than twice its time; with
+    stores of half lines it took nine times as long."""
+    n, rows, cols = 8, 20480, 128
+    codes, scales = vrc.vrc_mx4_quantize([torch.randn(rows, cols, device=DEV) for _ in range(n)])
+    shape = (n * rows, cols) if dim == 0 else (rows, n * cols)
+    times = {}
+    for dtype in ("bf16", "fp32"):
+        out = [torch.empty(shape, dtype=DT[dtype], device=DEV) for _ in range(n)]
+        times[dtype] = replay_us(lambda: vrc.vrc_mx4_all_gather(codes, scales, cols, dim=dim, dtype=DT[dtype], recv=out))
+    say(f"dim {dim}: {times}")
+    assert times["fp32"] < 4 * times["bf16"]
