@@ -612,14 +612,17 @@ int reduce_scatter_waves(int loads, uint64_t bytes)
 // flight per wave 4.4-4.8).
 constexpr int kGatherWaves = 64;
 
-// The workgroups of a call on chunks.  Where more elements go one by one than in
-// vectors, its time is theirs: a wave for every 64 of them, up to kScalarWaves per CU.
-constexpr int kScalarWaves = 32;
+// The workgroups of a call on chunks.  Where more waves of elements go one by one, or by
+// four in narrow rows, than in vectors, the call's time is theirs: up to 64 per CU (us
+// with 4 / 16 / 64, reduce-scatter: 8 x [16384, 8 x 47] fp16 50 / 29 / 29, 2 x [524288, 2 x
+// 7] bf16 36 / 19 / 16, 8 x [60000, 8 x 65] fp16 270 / 256 / 233, but 16 x [32768, 16 x 40]
+// bf16 180 / 169 / 182; all-gather: 52 / 35 / 33, 39 / 20 / 17, 235 / 156 / 156, 189 / 192 / 202).
+constexpr int kScalarWaves = 64;
 
 unsigned chunk_grid(const ChunkArgs& a, int cus, int per_cu)
 {
     const uint64_t tiles = a.tiles * (uint64_t)a.n, by_slots = (a.slots + 63) / 64;
-    return by_slots > tiles ? wave_grid(by_slots, cus, per_cu > kScalarWaves ? per_cu : kScalarWaves) : wave_grid(tiles, cus, per_cu);
+    return by_slots > tiles ? wave_grid(by_slots, cus, kScalarWaves) : wave_grid(tiles, cus, per_cu);
 }
 
 template <class T, int N, int RES>

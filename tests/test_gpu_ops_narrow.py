@@ -72,3 +72,18 @@ def test_narrow_rows_use_the_whole_card(vrc, width):  # noqa: F811
     say(f"width {width}: {times}")
     for narrow, wide in zip(times[outer], times[outer // 1024]):
         assert narrow < 6 * wide + 10
+
+
+def test_narrow_rows_past_32_bits(vrc):  # noqa: F811
+    n, outer, width = 2, (1 << 29) + 3, 4
+    total = outer * n * width
+    x = torch.ones(outer, n * width, dtype=torch.float16, device=DEV)
+    parts = vrc.vrc_reduce_scatter_dropout([x, x], 0.25, 77, 5, dim=1)
+    whole = vrc.vrc_all_gather_dropout(parts, 0.25, 77, 5, dim=1)
+    for row in (0, (1 << 28) - 2, (1 << 29) - 2, outer - 4):
+        k = ref.keep(row * n * width, 4 * n * width, 0.25, 77, 5).reshape(4, n, width)
+        for c in range(n):
+            assert ((parts[c][row:row + 4] != 0).cpu().numpy() == k[:, c]).all(), (row, c)
+        for w in whole:
+            assert ((w[row:row + 4] != 0).cpu().numpy() == k.reshape(4, -1)).all(), row
+    assert total > 1 << 32
