@@ -11,11 +11,13 @@
 // as zero codes with scale 1.
 //
 // Measured on MI355X, random codes: 8 x (4096 x 8192 x 4096) summed, eight bf16
-// outputs, 540 us (4.07 PFLOP/s; 107 us of it are the 537 MB of stores at the end of
-// each tile); 8192 x 8192 x 8192 253 us (4.34).  The matrix instructions alone,
-// operands from LDS but nothing loaded, take 213 us: random operands hold the
-// clock down (205 us whole on zeros), and 41 us of either are tile starts and
-// ends.  8 x (1 x 8192 x 4096) summed, a stream of 143 MB: 30.5 us, 4.7 TB/s.
+// outputs, 552 us with other operands at each call (3.98 PFLOP/s; 531 us with the same
+// ones; 107 us of it are the 537 MB of stores at the end of each tile; the matrix pipes
+// are busy for 53 % of all cycles); 8192 x 8192 x 8192 255 us (4.31).  The matrix
+// instructions alone, operands from LDS but nothing loaded, take 213 us: random operands
+// hold the clock down (205 us whole on zeros), and 41 us of either are tile starts and
+// ends.  8 x (1 x 8192 x 4096) summed, a stream of 143 MB: 27.0 us, 5.3 TB/s (28.6 us
+// under the profiler).
 #include <hip/hip_runtime.h>
 
 #include <utility>
@@ -438,8 +440,10 @@ __global__ __launch_bounds__(WM * WN * 64) void k_mx4_matmul_tiled(MatmulArgs a)
 // row's 16 scale bytes from any address and writes them to LDS itself.
 // Rows that do not start on a memory line have each tile's 128 bytes on two, twice
 // the CU's cache look-ups: 18 tiles each of 4 x (2048 x 1024), fp32 outputs, take 29.5
-// us whole, 34 us ragged and 43 us ragged with rows of 2064 bytes.  Reading the lines of
-// the tile after next ahead of time changes none of the three.
+// us whole, 34 us ragged and 43 us ragged with rows of 2064 bytes (4 x (2056 x 1000 x
+// 4100): 2.1 L2 requests for each row's 128 bytes, scales included, against 1.25 where
+// rows are whole).  Reading the lines of the tile after next ahead of time changes none
+// of the three.
 // ---------------------------------------------------------------------------
 template <int G>
 struct TurnsLds {
@@ -808,8 +812,8 @@ __global__ __launch_bounds__(WAVES * 64) void k_mx4_matmul_few(MatmulArgs a)
         }
     };
     // Two tiles ahead, without a branch around the loads: where some may not be under
-    // way, the compiler waits for all of them before each product (8 x (1 x 8192 x
-    // 4096) 32.5 us instead of 30.5, 4 x (1 x 5120 x 640) 5.3 instead of 4.3).  Three
+    // way, the compiler waits for all of them before each product (on one card 8 x (1 x
+    // 8192 x 4096) 32.5 us instead of 30.5, 4 x (1 x 5120 x 640) 5.3 instead of 4.3).  Three
     // tiles ahead or 16 waves gain nothing; loads that pass by the caches take 46 us,
     // as a row's line is read in four pieces.
     Frag<W, MI, WHOLE> f[2];
