@@ -48,7 +48,7 @@
 extern "C" {
 #endif
 
-#define VRC_OPS_VERSION 100 /* 1.0.0 */
+#define VRC_OPS_VERSION 101 /* 1.0.1: vrc_model.h's operators beside these */
 #define VRC_MX4_BLOCK 32    /* values that share a scale */
 
 typedef struct {

@@ -447,3 +447,8 @@ from .ops import *  # noqa: E402,F401,F403  (needs the names above)
 from .ops import __all__ as _ops_all  # noqa: E402
 
 __all__ += _ops_all
+
+from .model import *  # noqa: E402,F401,F403
+from .model import __all__ as _model_all  # noqa: E402
+
+__all__ += _model_all

@@ -16,12 +16,13 @@ LIB_OPS = os.path.join(PKG, "libvrc_ops.so")
 # holds the C ABI.  They compile in parallel.
 SOURCES = [os.path.join(CSRC, f) for f in
            ("vrc_type_bf16.hip", "vrc_type_f16.hip", "vrc_type_f32.hip", "vrc_type_i32.hip", "vrc_api.hip")]
-# The tensor-parallel layer's operators (include/vrc_ops.h) are a library of
+# The tensor-parallel layer's and model's operators (include/vrc_ops.h, vrc_model.h) are a library of
 # their own: libvrc.so's kernels only stream through registers, and its tests
 # pin that; these use LDS and the matrix cores.  They have a directory of their own
 # as well: the recorded counters of libvrc.so's kernels are tied to the bytes of csrc/.
 SOURCES_OPS = [os.path.join(CSRC_OPS, f) for f in
-               ("vrc_dropout.hip", "vrc_mx4_matmul.hip", "vrc_mx4.hip", "vrc_ops_api.hip")]
+               ("vrc_mx4_matmul.hip", "vrc_dropout.hip", "vrc_mx4.hip", "vrc_ops_api.hip", "vrc_cross_entropy_f32.hip",
+                "vrc_cross_entropy_f16.hip", "vrc_cross_entropy_bf16.hip", "vrc_layer_norm.hip", "vrc_model_api.hip")]
 OBJDIR = os.path.join(PKG, "_build")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

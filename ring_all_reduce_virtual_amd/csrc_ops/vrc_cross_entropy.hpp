@@ -1,0 +1,855 @@
+// vrc_cross_entropy.hpp -- kernels of the cross entropy over a split vocabulary
+// and of its gradient.  Internal; one unit per element type compiles them.
+//
+// Three products on the matrix cores (vrc_tiles.hpp), none of whose results leaves
+// the chip as logits:
+//   LOGITS   z = hidden W^T.  Its end is, for the loss, a maximum and a sum of
+//            exponentials of every row of a tile (and the target's logit from the one
+//            tile that has it), which a second launch joins; for the gradient, the
+//            tile of G = a exp(z - lse) - b [target], rounded to the type, of a piece
+//            of the vocabulary at a time;
+//   DWEIGHT  G^T hidden, whole for each row of the weights;
+//   DHIDDEN  G W, summed over the pieces (and over splits of the contraction, where
+//            there are few tiles) in fp32.
+// G is the only thing kept, [tokens, a piece's columns]; DHIDDEN reads it along its
+// rows, DWEIGHT across them.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "vrc_model_host.hpp"
+#include "vrc_tiles.hpp"
+
+namespace vrc {
+namespace {
+
+using host::EntropyCall;
+
+enum EntropyOp { kStats, kGrad, kDweight, kDhidden, kDsums };  // the last: DHIDDEN's sums, in fp32
+
+// A run of one rank's weight rows.
+struct Piece {
+    const char* w;       // its first row (packed or the caller's)
+    char* out;           // DWEIGHT: the first row's gradient
+    uint32_t len;        // rows
+    uint32_t first;      // of the whole vocabulary
+    uint32_t col;        // G: its first column, a multiple of 256
+    uint32_t tile;       // its first tile along the vocabulary, or (DHIDDEN) of the contraction
+};
+
+// A token's part of the gradient: a and b, scaled; lse; its target in the whole
+// vocabulary, or none.  Tokens without gradient have a = b = 0.
+struct Coef {
+    float a, b, lse;
+    uint32_t target;
+};
+constexpr uint32_t kNoTarget = 0xffffffffu;
+
+struct EntropyArgs {
+    Piece piece[kMaxRanks];
+    const char* a;        // LOGITS: hidden; else G
+    const char* b;        // DWEIGHT: hidden
+    uint64_t pitch_a, pitch_b, pitch_out;  // bytes of a row; pitch_b: of the weights', but for DWEIGHT
+    char* out;            // G, dhidden, or DHIDDEN's fp32 sums [split][token][pitch_out]
+    const Coef* coef;     // kGrad
+    const float* unscale; // what the products of G are multiplied by (null: nothing)
+    const long long* target;  // kStats
+    float2* stats;            // kStats: [tile along the vocabulary][token]
+    float* picked;            // kStats: [token]
+    uint32_t tiles_m, tiles_n;
+    uint32_t tokens, rows_a, width, granules;  // rows_a: rows that LOGITS and DHIDDEN read of A; granules: of a row of B (across)
+    uint32_t ktiles;          // of the contraction
+    uint32_t kwidth;          // LOGITS: elements of the contraction; DWEIGHT: whole tiles of it
+    int pieces;
+    int first_piece;          // DHIDDEN to fp32 sums: this launch is the first
+};
+
+// Four consecutive columns, rounded.
+template <class T>
+struct Quad {
+    uint32_t w[T::ESZ];
+    __device__ __forceinline__ explicit Quad(const float* v)
+    {
+        if constexpr (T::ESZ == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; i++) w[i] = (uint32_t)T::narrow(v[2 * i]) | (uint32_t)T::narrow(v[2 * i + 1]) << 16;
+        }
+    }
+};
+
+// A wave's results to sink(row, column, 16 bytes), 32 rows at a time through `own`,
+// the wave's part of LDS, so that they leave along the rows.  value(i, j, e): result e of
+// the instruction tile (i, j).  Row r's 16-byte piece c is at c ^ (r mod 8) (mod 4 where
+// a row has four), which spreads a column over the banks.
+template <class T, int MI, int NI, class Value, class Sink>
+__device__ __forceinline__ void drain(char* own, uint32_t lane, Value value, Sink sink)
+{
+    constexpr uint32_t PITCH = NI * 32 * T::ESZ, VECS = NI * 32 / T::VEC, MIX = VECS < 8 ? VECS - 1 : 7;
+    const uint32_t r = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < MI; i++) {
+#pragma unroll
+        for (int j = 0; j < NI; j++)
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[e] = value(i, j, 4 * g + e);
+                const Quad<T> f(v);
+                if constexpr (T::ESZ == 4)
+                    *(u32x4*)(own + r * PITCH + ((j * 8 + 2 * g + half) ^ (r & MIX)) * 16) = u32x4{f.w[0], f.w[1], f.w[2], f.w[3]};
+                else
+                    *(u32x2*)(own + r * PITCH + ((j * 4 + g) ^ (r & MIX)) * 16 + half * 8) = u32x2{f.w[0], f.w[1]};
+            }
+        __builtin_amdgcn_wave_barrier();
+        for (uint32_t v = lane; v < 32 * VECS; v += 64)
+            sink(i * 32 + v / VECS, v % VECS * T::VEC, *(const u32x4*)(own + v / VECS * PITCH + ((v % VECS) ^ (v / VECS & MIX)) * 16));
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// `left` (1 to VEC and more) elements of x to `to`, at any element's address.
+template <class T>
+__device__ __forceinline__ void store_some(char* to, u32x4 x, uint32_t left)
+{
+    if (left >= T::VEC) {
+        st16<false>(to, x);
+        return;
+    }
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < T::VEC; e++)
+        if (e < (int)left) store_s<T>(to + e * T::ESZ, (typename T::S)(T::ESZ == 4 ? w[e % 4] : w[e / 2 % 4] >> (16 * (e & 1))));
+}
+
+// exp(x) for x <= 0 (or NaN): the hardware's 2^x, whose error and that of the product
+// before it are below half a step of a 16-bit result by far; fp32's own for fp32.
+template <class T>
+__device__ __forceinline__ float exp_of(float x)
+{
+    if constexpr (T::ESZ == 4) return expf(x);
+    else return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
+}
+
+// A workgroup of WM x WN waves has a BM x BN tile of the result, a wave MI x NI
+// matrix-instruction tiles of it.  A ring of S stages, up to S - 1 tiles of the
+// contraction ahead; one barrier a tile, behind which its loads have landed for
+// every wave and the stage of the tile before it is free.  Past the last tile the
+// loop goes on fetching that tile again, so that every wave always has the same number of
+// loads under way, which is what its waits count.
+// CUT: B's elements past the end of the contraction are read from a constant zero
+// (A's are zero in memory, or are multiplied by those).
+template <class T, int OP, int BM, int BN, int WM, int WN, int S, bool CUT>
+__global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
+{
+    constexpr int MI = BM / WM / 32, NI = BN / WN / 32, WAVES = WM * WN;
+    constexpr bool DHIDDEN = OP == kDhidden || OP == kDsums;
+    typedef TileOperand<T, OP == kDweight ? kAcross : kAlong, BM> A;
+    typedef TileOperand<T, OP == kStats || OP == kGrad ? kAlong : kAcross, BN> B;
+    constexpr uint32_t LOADS = (A::LOADS + B::LOADS) / WAVES, STAGE = A::BYTES + B::BYTES, KT = kTileK<T>;
+    static_assert((A::LOADS + B::LOADS) % WAVES == 0 && S >= 2 && LOADS * (S - 1) < 64, "loads are shared out evenly");
+    __shared__ __attribute__((aligned(16))) char ring[S][STAGE];
+
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    uint32_t tm, tn;
+    xcd_tile<4>(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
+
+    // The piece of the vocabulary, and the tile's first row and column in it.
+    uint32_t m0 = tm * BM, n0 = tn * BN;
+    int p = 0;
+    if constexpr (!DHIDDEN) {
+        const uint32_t t = OP == kDweight ? tm : tn;
+        while (p + 1 < a.pieces && t >= a.piece[p + 1].tile) p++;
+        if constexpr (OP == kDweight) m0 = (tm - a.piece[p].tile) * BM;
+        else n0 = (tn - a.piece[p].tile) * BN;
+    }
+    uint32_t t0 = 0, total = a.ktiles;
+    if constexpr (DHIDDEN) {  // this split's tiles
+        const uint64_t splits = gridDim.y;
+        t0 = (uint32_t)(a.ktiles * (uint64_t)blockIdx.y / splits);
+        total = (uint32_t)(a.ktiles * (uint64_t)(blockIdx.y + 1) / splits) - t0;
+        while (p + 1 < a.pieces && t0 >= a.piece[p + 1].tile) p++;
+    }
+
+    // This lane's part of each of its wave's loads.
+    uint32_t off[LOADS], kk[LOADS];
+#pragma unroll
+    for (uint32_t i = 0; i < LOADS; i++) {
+        const uint32_t at = wave * LOADS + i;
+        if (at < A::LOADS) {
+            // across: a piece's columns of G are there up to a multiple of 256
+            const uint32_t last = OP == kDweight ? 0xffffffffu : a.rows_a - 1 - m0;
+            A::source(at * 64 + lane, (uint32_t)a.pitch_a, last, off[i], kk[i]);
+            kk[i] = 0;
+        } else {
+            const uint32_t last = OP == kStats || OP == kGrad ? a.piece[p].len - 1 - n0 : a.granules - 1 - n0 * T::ESZ / 16;
+            B::source((at - A::LOADS) * 64 + lane, (uint32_t)a.pitch_b, last, off[i], kk[i]);
+        }
+    }
+    uint32_t kt = t0, fetched = 0, fstage = 0;  // kt: of the tile that is fetched next
+    const auto fetch = [&] {
+        const char *pa, *pb;
+        uint32_t left = ~0u;
+        if constexpr (DHIDDEN) {
+            const Piece& q = a.piece[p];
+            const uint32_t k = (kt - q.tile) * KT;
+            pa = a.a + m0 * a.pitch_a + (uint64_t)(q.col + k) * T::ESZ;
+            pb = q.w + (uint64_t)k * a.pitch_b + (uint64_t)n0 * T::ESZ;
+            left = q.len - k;
+        } else if constexpr (OP == kDweight) {
+            pa = a.a + (uint64_t)(a.piece[p].col + m0) * T::ESZ + (uint64_t)kt * KT * a.pitch_a;
+            pb = a.b + (uint64_t)n0 * T::ESZ + (uint64_t)kt * KT * a.pitch_b;
+        } else {
+            pa = a.a + m0 * a.pitch_a + (uint64_t)kt * kTileRow;
+            pb = a.piece[p].w + n0 * a.pitch_b + (uint64_t)kt * kTileRow;
+            left = a.kwidth - kt * KT;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < LOADS; i++) {
+            const uint32_t at = wave * LOADS + i;
+            auto from = (global_ptr<const char>)(at < A::LOADS ? pa : pb) + hidden_offset(off[i]);
+            if constexpr (CUT)
+                if (kk[i] >= left) from = (global_ptr<const char>)&kZeroGranule;
+            granules_to_lds(from, ring[fstage] + at * 1024);
+        }
+        fstage = fstage + 1 == S ? 0 : fstage + 1;
+        fetched++;
+        if (fetched < total) {
+            kt++;
+            if constexpr (DHIDDEN) p += p + 1 < a.pieces && kt >= a.piece[p + 1].tile;
+        }
+    };
+
+    f32x16 acc[MI][NI] = {};
+    const uint32_t wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN), r = lane & 31, half = lane >> 5;
+    if (total) {
+#pragma unroll
+        for (int t = 0; t + 1 < S; t++) fetch();
+        uint32_t cur = 0;
+        for (uint32_t t = 0; t < total; t++) {
+            wait_vmem_below<LOADS*(S - 2)>();
+            tile_barrier();
+            fetch();
+            const char* stage = ring[cur];
+            cur = cur + 1 == S ? 0 : cur + 1;
+#pragma unroll
+            for (int s = 0; s < 4; s++) {
+                u32x4 x[MI], y[NI];
+#pragma unroll
+                for (int j = 0; j < NI; j++) y[j] = B::read(stage + A::BYTES, wn + j * 32, s, lane);
+#pragma unroll
+                for (int i = 0; i < MI; i++) x[i] = A::read(stage, wm + i * 32, s, lane);
+#pragma unroll
+                for (int i = 0; i < MI; i++)
+#pragma unroll
+                    for (int j = 0; j < NI; j++) acc[i][j] = tile_mfma<T>(y[j], x[i], acc[i][j]);
+            }
+        }
+        wait_vmem_below<0>();
+    }
+    __syncthreads();
+
+    if constexpr (OP == kStats) {
+        const uint32_t cols = a.piece[p].len - n0;  // that the tile has
+        float2* const part = (float2*)&ring[0][0];  // [WN][BM]
+#pragma unroll
+        for (int i = 0; i < MI; i++) {
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NI; j++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    if (wn + j * 32 + result_col(e, half) >= cols) acc[i][j][e] = -INFINITY;
+                    top = fmaxf(top, acc[i][j][e]);
+                }
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            // rows of infinities: differences from 0 instead, whose exponentials are 0 and infinity
+            const float from = __builtin_isinf(top) ? 0.0f : top;
+#pragma unroll
+            for (int j = 0; j < NI; j++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) sum += exp_of<T>(acc[i][j][e] - from);
+            sum += __shfl_xor(sum, 32, 64);
+            if (half == 0) part[wave / WM * BM + wm + i * 32 + r] = make_float2(top, sum);
+            const uint32_t token = m0 + wm + i * 32 + r;
+            if (a.target && token < a.tokens) {
+                const unsigned long long at = (unsigned long long)a.target[token] - a.piece[p].first - n0 - wn;
+                if (at < BN / WN && wn + at < cols) {
+                    float z = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NI; j++)
+#pragma unroll
+                        for (int e = 0; e < 16; e++) z = j * 32 + result_col(e, half) == at ? acc[i][j][e] : z;
+                    if ((at >> 2 & 1) == half) a.picked[token] = z;
+                }
+            }
+        }
+        __syncthreads();
+        for (uint32_t m = tid; m < BM; m += WAVES * 64) {
+            if (m0 + m >= a.tokens) continue;
+            float top = part[m].x;
+#pragma unroll
+            for (int w = 1; w < WN; w++) top = fmaxf(top, part[w * BM + m].x);
+            const float from = __builtin_isinf(top) ? 0.0f : top;
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WN; w++) {
+                const float2 v = part[w * BM + m];
+                sum += v.y * exp_of<T>(v.x - from);
+            }
+            a.stats[(uint64_t)tn * a.tokens + m0 + m] = make_float2(top, sum);
+        }
+    } else {
+        constexpr uint32_t PART = 32 * NI * 32;  // results of a wave on their way out
+        if constexpr (OP == kGrad) {
+            static_assert(WAVES * PART * T::ESZ <= S * STAGE, "the results' way out fits the ring");
+            const uint32_t cols = a.piece[p].len - n0;
+            Coef c[MI];
+#pragma unroll
+            for (int i = 0; i < MI; i++) {
+                const uint32_t token = m0 + wm + i * 32 + r;
+                c[i] = a.coef[token < a.rows_a ? token : a.rows_a - 1];
+                c[i].target -= a.piece[p].first + n0 + wn;
+            }
+            drain<T, MI, NI>(&ring[0][0] + wave * PART * T::ESZ, lane,
+                [&](int i, int j, int e) {
+                    const uint32_t col = j * 32 + result_col(e, half);
+                    float g = c[i].a * exp_of<T>(acc[i][j][e] - c[i].lse);
+                    g = col == c[i].target ? g - c[i].b : g;
+                    return (c[i].a == 0.0f && c[i].b == 0.0f) || wn + col >= cols ? 0.0f : g;
+                },
+                [&](uint32_t row, uint32_t col, u32x4 x) {
+                    const uint32_t token = m0 + wm + row;
+                    if (token < a.rows_a) st16<false>(a.out + token * a.pitch_out + (uint64_t)(a.piece[p].col + n0 + wn + col) * T::ESZ, x);
+                });
+        } else if constexpr (OP == kDsums) {
+            static_assert(WAVES * PART * 4 <= S * STAGE, "the results' way out fits the ring");
+            char* const out = a.out + blockIdx.y * (uint64_t)a.tokens * a.pitch_out;
+            drain<F32, MI, NI>(&ring[0][0] + wave * PART * 4, lane, [&](int i, int j, int e) { return acc[i][j][e]; },
+                [&](uint32_t row, uint32_t col, u32x4 x) {
+                    const uint64_t m = m0 + wm + row;
+                    const uint32_t n = n0 + wn + col;
+                    if (m >= a.tokens || n >= a.width) return;  // rows of sums are padded to whole vectors
+                    char* const to = out + m * a.pitch_out + (uint64_t)n * 4;
+                    if (!a.first_piece) {
+                        const u32x4 old = ld16<false>(to);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) x[e] = __float_as_uint(__uint_as_float(old[e]) + __uint_as_float(x[e]));
+                    }
+                    st16<false>(to, x);
+                });
+        } else {
+            const float u = a.unscale ? *a.unscale : 1.0f;
+            const uint32_t rows = OP == kDweight ? a.piece[p].len : a.tokens;
+            char* const out = OP == kDweight ? a.piece[p].out : a.out;
+            static_assert(WAVES * PART * T::ESZ <= S * STAGE, "the results' way out fits the ring");
+            drain<T, MI, NI>(&ring[0][0] + wave * PART * T::ESZ, lane, [&](int i, int j, int e) { return acc[i][j][e] * u; },
+                [&](uint32_t row, uint32_t col, u32x4 x) {
+                    const uint64_t m = m0 + wm + row;
+                    const uint32_t n = n0 + wn + col;
+                    if (m < rows && n < a.width) store_some<T>(out + m * a.pitch_out + (uint64_t)n * T::ESZ, x, a.width - n);
+                });
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// What stands around the products.
+// ---------------------------------------------------------------------------
+
+// A sum over a workgroup of 256, in every lane.
+__device__ __forceinline__ float group_max(float v, float* lds)
+{
+#pragma unroll
+    for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lds[0];
+    for (uint32_t w = 1; w < blockDim.x / 64; w++) v = fmaxf(v, lds[w]);
+    return v;
+}
+
+__device__ __forceinline__ float group_sum(float v, float* lds)
+{
+#pragma unroll
+    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lds[0];
+    for (uint32_t w = 1; w < blockDim.x / 64; w++) v += lds[w];
+    return v;
+}
+
+// The tiles' maxima and sums of one token, joined by TOKENS lanes' columns: 256 lanes
+// are 16 tokens by 16 runs of tiles (neighbouring lanes read neighbouring tokens).
+__global__ __launch_bounds__(256) void k_entropy_loss(const float2* stats, const float* picked, uint32_t tiles, uint32_t tokens,
+                                                      const long long* target, long long ignore, uint32_t vocab, float* loss,
+                                                      float* lse)
+{
+    __shared__ float2 part[16][17];
+    const uint32_t c = threadIdx.x % 16, run = threadIdx.x / 16, token = blockIdx.x * 16 + c;
+    float top = -INFINITY, sum = 0.0f;
+    if (token < tokens) {
+        for (uint32_t i = run; i < tiles; i += 16) top = fmaxf(top, stats[(uint64_t)i * tokens + token].x);
+        const float from = __builtin_isinf(top) ? 0.0f : top;
+        for (uint32_t i = run; i < tiles; i += 16) {
+            const float2 v = stats[(uint64_t)i * tokens + token];
+            sum += v.y * expf(v.x - from);
+        }
+    }
+    part[run][c] = make_float2(top, sum);
+    __syncthreads();
+    if (run || token >= tokens) return;
+    for (int q = 1; q < 16; q++) top = fmaxf(top, part[q][c].x);
+    const float from = __builtin_isinf(top) ? 0.0f : top;
+    sum = 0.0f;
+    for (int q = 0; q < 16; q++) sum += part[q][c].y * expf(part[q][c].x - from);
+    const float l = from + logf(sum);
+    lse[token] = l;
+    if (!loss) return;
+    const long long t = target[token];
+    loss[token] = t == ignore ? 0.0f : (unsigned long long)t < vocab ? l - picked[token] : __builtin_nanf("");
+}
+
+// The tokens' coefficients, by one workgroup.  16-bit G is held in units of the largest
+// |a| or |b| (fp16: 2^-14 of it): the targets' elements of a loss whose tokens weigh
+// the same are then rounded from 1 - p instead of from an arbitrary weight, and fp16's
+// small range does not matter.  scale[0]: one such unit.
+template <class T>
+__global__ __launch_bounds__(1024) void k_entropy_coef(const long long* target, const float* lse, const float* dloss,
+                                                       const float* dlse, long long ignore, uint32_t vocab, uint32_t tokens,
+                                                       uint32_t padded, Coef* coef, float* scale)
+{
+    __shared__ float lds[16];
+    const auto of = [&](uint32_t t) {
+        const long long at = target[t];
+        const bool none = at == ignore, bad = !none && (unsigned long long)at >= vocab;
+        Coef c;
+        c.b = none ? 0.0f : dloss[t];
+        c.a = c.b + (dlse ? dlse[t] : 0.0f);
+        if (bad) c.a = __builtin_nanf("");
+        c.lse = lse[t];
+        c.target = none || bad ? kNoTarget : (uint32_t)at;
+        return c;
+    };
+    float unit = 1.0f, up = 1.0f;
+    if constexpr (T::ESZ == 2) {
+        float most = 0.0f;
+        for (uint32_t t = threadIdx.x; t < tokens; t += 1024) {
+            const Coef c = of(t);
+            const float x = fmaxf(fabsf(c.a), fabsf(c.b));
+            most = fmaxf(most, __builtin_isfinite(x) ? x : 0.0f);
+        }
+        most = group_max(most, lds);
+        // between 2^-100 and 2^100, where neither the unit nor its inverse leaves fp32's range
+        most = most == 0.0f ? 1.0f : fminf(fmaxf(most, 0x1p-100f), 0x1p100f);
+        unit = __is_same(T, F16) ? most * 0x1p-14f : most;
+        up = 1.0f / unit;
+    }
+    for (uint32_t t = threadIdx.x; t < padded; t += 1024) {
+        Coef c = {0.0f, 0.0f, 0.0f, kNoTarget};
+        if (t < tokens) {
+            c = of(t);
+            c.a *= up;
+            c.b *= up;
+        }
+        coef[t] = c;
+    }
+    if (threadIdx.x == 0) scale[0] = unit;
+}
+
+// Rows of a matrix at a pitch of whole tiles, zero behind each row's end, behind the
+// last row and (where coef is given) in rows of tokens without gradient: what those hold
+// then reaches no product.
+template <class T>
+__global__ __launch_bounds__(256) void k_entropy_pack(const char* src, char* dst, uint32_t rows, uint32_t padded, uint32_t width,
+                                                      uint32_t granules, const Coef* coef)
+{
+    for (uint32_t row = blockIdx.x; row < padded; row += gridDim.x) {
+        bool live = row < rows;
+        if (live && coef) live = coef[row].a != 0.0f || coef[row].b != 0.0f;
+        const char* from = src + (uint64_t)row * width * T::ESZ;
+        for (uint32_t g = threadIdx.x; g < granules; g += 256) {
+            const uint32_t col = g * T::VEC;
+            u32x4 x = {0, 0, 0, 0};
+            if (live && col < width) {
+                if (col + T::VEC <= width) {
+                    x = ld16<false>(from + (uint64_t)g * 16);
+                } else {
+                    uint32_t w[4] = {0, 0, 0, 0};
+                    for (uint32_t e = 0; col + e < width; e++) {
+                        const uint32_t s = load_s<T>(from + (uint64_t)(col + e) * T::ESZ);
+                        if constexpr (T::ESZ == 4) w[e] = s;
+                        else w[e / 2] |= s << (16 * (e & 1));
+                    }
+                    x = u32x4{w[0], w[1], w[2], w[3]};
+                }
+            }
+            st16<false>(dst + ((uint64_t)row * granules + g) * 16, x);
+        }
+    }
+}
+
+// out = unscale x the splits' sums, in their order, rounded.
+template <class T>
+__global__ __launch_bounds__(256) void k_entropy_join(const float* sums, uint32_t splits, uint32_t tokens, uint32_t width,
+                                                      uint32_t pitch, const float* unscale, char* out)
+{
+    const float u = *unscale;
+    const uint32_t quads = (width + 3) / 4;
+    for (uint32_t row = blockIdx.y; row < tokens; row += gridDim.y)
+        for (uint32_t q = blockIdx.x * 256 + threadIdx.x; q < quads; q += gridDim.x * 256) {
+            float s[4] = {};
+            for (uint32_t i = 0; i < splits; i++) {
+                float v[4];
+                F32::unpack(ld16<false>((const char*)(sums + ((uint64_t)i * tokens + row) * pitch + q * 4)), v);
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[e] += v[e];
+            }
+            char* const to = out + ((uint64_t)row * width + q * 4) * T::ESZ;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (q * 4 + e < width) store_s<T>(to + e * T::ESZ, T::narrow(s[e] * u));
+        }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void k_entropy_zero(char* out, uint64_t count)
+{
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < count; i += gridDim.x * 256ull) store_s<T>(out + i * T::ESZ, 0);
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+using namespace host;
+
+constexpr uint64_t kCus = 256;               // of the card this library is built for; plans do not ask the device
+constexpr uint64_t kPieceBytes = 128u << 20; // G of one piece of the vocabulary, and packed weights: half the last-level cache
+
+inline uint64_t up_to(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
+
+// What one call does, from its sizes and alignments alone, so that the workspace's
+// size can be asked for beforehand.
+template <class T>
+struct EntropyPlan {
+    static constexpr uint64_t KT = kTileK<T>;
+    uint64_t vocab = 0, columns = 0;  // the whole; the same with each rank's rounded up to 256
+    uint64_t padded, wide;            // tokens rounded up to 64; elements of a packed row
+    bool pack_hidden, pack_weight, cut;
+    uint64_t piece;                   // columns of a piece at most, a multiple of 256
+    uint64_t tokens;                  // of one pass (the loss)
+    int splits = 1;                   // of DHIDDEN's contraction
+    bool sums = false;                // whether DHIDDEN goes by fp32 sums
+    uint64_t at_hidden = 0, at_weight = 0, at_stats = 0, at_picked = 0, at_coef = 0, at_scale = 0, at_g = 0, at_sums = 0, bytes = 0;
+
+    uint64_t take(uint64_t size)
+    {
+        const uint64_t at = bytes;
+        bytes += up_to(size, 256);
+        return at;
+    }
+    static bool direct(uint64_t width, uintptr_t p) { return width * T::ESZ % 16 == 0 && p % 16 == 0; }
+    uint64_t pieces_of(uint64_t piece_columns) const { return (columns + piece_columns - 1) / piece_columns; }
+
+    EntropyPlan(const EntropyCall& c, bool gradient)
+    {
+        pack_weight = false;
+        for (int r = 0; r < c.n; r++) {
+            vocab += c.vocab[r];
+            columns += up_to(c.vocab[r], 256);
+            if (c.vocab[r]) pack_weight |= !direct(c.width, (uintptr_t)c.weight[r]);
+        }
+        wide = up_to(c.width, KT);
+        padded = up_to(c.tokens ? c.tokens : 1, 64);
+        cut = c.width % KT != 0 && !pack_weight;
+        // the gradient's hidden states are always packed: rows of tokens without gradient are zero
+        pack_hidden = gradient ? true : c.width % KT != 0 || !direct(c.width, (uintptr_t)c.hidden);
+        piece = up_to(columns, 256);
+        if (pack_weight) piece = limit(piece, kPieceBytes / (wide * T::ESZ), 256);
+        tokens = c.tokens;
+        if (!gradient) {
+            tokens = c.tokens < 16384 ? c.tokens : 16384;
+            if (pack_hidden) at_hidden = take(c.tokens * wide * T::ESZ);
+            if (pack_weight) at_weight = take(piece * wide * T::ESZ);
+            at_stats = take((columns / 128) * tokens * sizeof(float2));
+            at_picked = take(tokens * sizeof(float));
+            return;
+        }
+        if (columns == 0) return;
+        // pieces of a few thousand columns at least, so that the sums over them cost little
+        piece = limit(piece, kPieceBytes / (padded * T::ESZ), 4096);
+        piece = up_to((columns + pieces_of(piece) - 1) / pieces_of(piece), 256);  // of about one size
+        at_coef = take(padded * sizeof(Coef));
+        at_scale = take(16);
+        at_hidden = take(padded * wide * T::ESZ);
+        if (pack_weight) at_weight = take(piece * wide * T::ESZ);
+        at_g = take(padded * pitch_g());
+        if (c.want_dhidden) {
+            // few tiles: the contraction is split until there are about two a CU
+            const uint64_t bm = c.tokens <= 32 ? 32 : c.tokens <= 64 ? 64 : c.tokens <= 128 ? 128 : 256, bn = bm == 256 ? 256 : 128;
+            const uint64_t tiles = ((c.tokens + bm - 1) / bm) * ((c.width + bn - 1) / bn);
+            uint64_t s = tiles >= kCus * 3 / 4 ? 1 : (2 * kCus + tiles - 1) / tiles;
+            const uint64_t most = piece / KT / 4;  // of four tiles at least
+            s = s < most ? s : most;
+            splits = s < 1 ? 1 : s > 128 ? 128 : (int)s;
+            sums = splits > 1 || pieces_of(piece) > 1;
+            if (sums) at_sums = take((uint64_t)splits * c.tokens * wide * sizeof(float));
+        }
+    }
+    // At most `most` columns (rounded down to 256), but no fewer than `least`.
+    static uint64_t limit(uint64_t piece, uint64_t most, uint64_t least)
+    {
+        most = most / 256 * 256;
+        most = most > least ? most : least;
+        return piece < most ? piece : most;
+    }
+    // A row of G: 128 bytes more than its columns, so that rows start on other memory channels.
+    uint64_t pitch_g() const { return piece * T::ESZ + 128; }
+};
+
+// The pieces of the vocabulary, a few at a time: `columns` of them at most.
+struct PieceWalk {
+    const EntropyCall& c;
+    uint64_t columns;
+    int r = 0;
+    uint64_t at = 0;     // of rank r's rows
+    uint64_t first = 0;  // of the whole vocabulary
+
+    // The next launch's pieces; tile sizes are set by the caller.
+    int next(Piece* piece, int esz)
+    {
+        int n = 0;
+        uint64_t col = 0;
+        while (r < c.n && col < columns && n < kMaxRanks) {
+            const uint64_t left = c.vocab[r] - at, room = columns - col;
+            if (left == 0) {
+                r++;
+                at = 0;
+                continue;
+            }
+            const uint64_t len = left < room ? left : room, row = c.width * (uint64_t)esz;
+            Piece& q = piece[n++];
+            q = {};
+            q.w = c.weight[r] + at * row;
+            q.out = c.dweight[r] ? c.dweight[r] + at * row : nullptr;
+            q.len = (uint32_t)len;
+            q.first = (uint32_t)first;
+            q.col = (uint32_t)col;
+            col += up_to(len, 256);
+            first += len;
+            at += len;
+        }
+        return n;
+    }
+};
+
+template <class T, int OP, int BM, int BN, int WM, int WN, int S>
+vrc_status_t launch_entropy(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut, int splits, hipStream_t st)
+{
+    a.tiles_m = (uint32_t)((rows + BM - 1) / BM);
+    a.tiles_n = (uint32_t)((cols + BN - 1) / BN);
+    constexpr bool DHIDDEN = OP == kDhidden || OP == kDsums;
+    if constexpr (DHIDDEN) {
+        uint32_t t = 0;
+        for (int i = 0; i < a.pieces; i++) {
+            a.piece[i].tile = t;
+            t += (uint32_t)((a.piece[i].len + kTileK<T> - 1) / kTileK<T>);
+        }
+        a.ktiles = t;
+    } else {
+        constexpr uint32_t B = OP == kDweight ? BM : BN;
+        uint32_t t = 0;
+        for (int i = 0; i < a.pieces; i++) {
+            a.piece[i].tile = t;
+            t += (a.piece[i].len + B - 1) / B;
+        }
+        (OP == kDweight ? a.tiles_m : a.tiles_n) = t;
+    }
+    const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
+    if (tiles * (WM * WN * 64) > 0xffffffffull) return VRC_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)tiles, (unsigned)splits);
+    if constexpr (OP == kDweight) {
+        k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
+    } else if constexpr (DHIDDEN) {
+        k_entropy<T, OP, BM, BN, WM, WN, S, true><<<grid, WM * WN * 64, 0, st>>>(a);
+    } else {
+        if (cut) k_entropy<T, OP, BM, BN, WM, WN, S, true><<<grid, WM * WN * 64, 0, st>>>(a);
+        else k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
+    }
+    return check_launch();
+}
+
+// Tiles by the rows of the result (tokens; for DWEIGHT the vocabulary's).
+template <class T, int OP>
+vrc_status_t launch_by_rows(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut, int splits, hipStream_t st)
+{
+    if constexpr (OP != kDweight) {
+        if (a.tokens <= 32) return launch_entropy<T, OP, 32, 128, 1, 4, 4>(a, rows, cols, cut, splits, st);
+        if (a.tokens <= 64) return launch_entropy<T, OP, 64, 128, 1, 4, 3>(a, rows, cols, cut, splits, st);
+        if (a.tokens <= 128) return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
+    } else {
+        if (a.tokens <= 128) return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
+    }
+    return launch_entropy<T, OP, 256, 256, 2, 4, 2>(a, rows, cols, cut, splits, st);
+}
+
+template <class T>
+vrc_status_t pack(const char* src, char* dst, uint64_t rows, uint64_t padded, uint64_t width, uint64_t wide, const Coef* coef,
+                  hipStream_t st)
+{
+    if (padded == 0) return VRC_OK;
+    k_entropy_pack<T><<<(unsigned)(padded < 65536 ? padded : 65536), 256, 0, st>>>(src, dst, (uint32_t)rows, (uint32_t)padded, (uint32_t)width,
+                                                                              (uint32_t)(wide * T::ESZ / 16), coef);
+    return check_launch();
+}
+
+// The launch's pieces in the packed form.
+template <class T>
+vrc_status_t pack_pieces(const EntropyCall& c, const EntropyPlan<T>& plan, EntropyArgs& a, hipStream_t st)
+{
+    char* to = c.workspace + plan.at_weight;
+    for (int i = 0; i < a.pieces; i++) {
+        const vrc_status_t rc = pack<T>(a.piece[i].w, to, a.piece[i].len, a.piece[i].len, c.width, plan.wide, nullptr, st);
+        if (rc) return rc;
+        a.piece[i].w = to;
+        to += (uint64_t)a.piece[i].len * plan.wide * T::ESZ;
+    }
+    return VRC_OK;
+}
+
+template <class T>
+vrc_status_t cross_entropy_typed(const EntropyCall& c, hipStream_t st)
+{
+    const EntropyPlan<T> plan(c, false);
+    const char* hidden = c.hidden;
+    if (plan.pack_hidden) {
+        char* const to = c.workspace + plan.at_hidden;
+        const vrc_status_t rc = pack<T>(c.hidden, to, c.tokens, c.tokens, c.width, plan.wide, nullptr, st);
+        if (rc) return rc;
+        hidden = to;
+    }
+    float2* const stats = (float2*)(c.workspace + plan.at_stats);
+    float* const picked = (float*)(c.workspace + plan.at_picked);
+    for (uint64_t t0 = 0; t0 < c.tokens; t0 += plan.tokens) {
+        const uint64_t tokens = c.tokens - t0 < plan.tokens ? c.tokens - t0 : plan.tokens;
+        uint64_t tiles = 0;
+        PieceWalk walk = {c, plan.piece};
+        EntropyArgs a = {};
+        while ((a.pieces = walk.next(a.piece, T::ESZ)) != 0) {
+            if (plan.pack_weight) {
+                const vrc_status_t rc = pack_pieces(c, plan, a, st);
+                if (rc) return rc;
+            }
+            a.pitch_a = (plan.pack_hidden ? plan.wide : c.width) * T::ESZ;
+            a.pitch_b = (plan.pack_weight ? plan.wide : c.width) * T::ESZ;
+            a.a = hidden + t0 * a.pitch_a;
+            a.target = c.loss ? c.target + t0 : nullptr;
+            a.stats = stats + tiles * tokens;
+            a.picked = picked;
+            a.tokens = a.rows_a = (uint32_t)tokens;
+            a.kwidth = (uint32_t)c.width;
+            a.ktiles = (uint32_t)(plan.wide / plan.KT);
+            const vrc_status_t rc = launch_by_rows<T, kStats>(a, tokens, 0, plan.cut, 1, st);
+            if (rc) return rc;
+            tiles += a.tiles_n;
+        }
+        k_entropy_loss<<<(unsigned)((tokens + 15) / 16), 256, 0, st>>>(stats, picked, (uint32_t)tiles, (uint32_t)tokens,
+                                                                       c.loss ? c.target + t0 : nullptr, c.ignore_index,
+                                                                       (uint32_t)plan.vocab, c.loss ? c.loss + t0 : nullptr, c.lse + t0);
+        const vrc_status_t rc = check_launch();
+        if (rc) return rc;
+    }
+    return VRC_OK;
+}
+
+template <class T>
+vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
+{
+    const EntropyPlan<T> plan(c, true);
+    if (plan.columns == 0) {  // nothing to add up
+        if (c.want_dhidden) {
+            const uint64_t count = c.tokens * c.width, groups = (count + 255) / 256;
+            k_entropy_zero<T><<<(unsigned)(groups < 65536 ? groups : 65536), 256, 0, st>>>(c.dhidden, count);
+            return check_launch();
+        }
+        return VRC_OK;
+    }
+    Coef* const coef = (Coef*)(c.workspace + plan.at_coef);
+    float* const scale = (float*)(c.workspace + plan.at_scale);
+    char* const hidden = c.workspace + plan.at_hidden;
+    char* const g = c.workspace + plan.at_g;
+    char* const sums = c.workspace + plan.at_sums;
+    k_entropy_coef<T><<<1, 1024, 0, st>>>(c.target, c.lse, c.dloss, c.dlse, c.ignore_index, (uint32_t)plan.vocab,
+                                          (uint32_t)c.tokens, (uint32_t)plan.padded, coef, scale);
+    vrc_status_t rc = check_launch();
+    if (rc) return rc;
+    rc = pack<T>(c.hidden, hidden, c.tokens, plan.padded, c.width, plan.wide, coef, st);
+    if (rc) return rc;
+
+    EntropyArgs a = {};
+    PieceWalk walk = {c, plan.piece};
+    bool first = true;
+    while ((a.pieces = walk.next(a.piece, T::ESZ)) != 0) {
+        if (plan.pack_weight) {
+            rc = pack_pieces(c, plan, a, st);
+            if (rc) return rc;
+        }
+        const uint64_t pitch_w = (plan.pack_weight ? plan.wide : c.width) * T::ESZ;
+        a.tokens = (uint32_t)c.tokens;
+        a.width = (uint32_t)c.width;
+        a.rows_a = (uint32_t)plan.padded;
+        // G
+        a.a = hidden;
+        a.pitch_a = plan.wide * T::ESZ;
+        a.pitch_b = pitch_w;
+        a.kwidth = a.width;
+        a.ktiles = (uint32_t)(plan.wide / plan.KT);
+        a.coef = coef;
+        a.out = g;
+        a.pitch_out = plan.pitch_g();
+        rc = launch_by_rows<T, kGrad>(a, plan.padded, 0, plan.cut, 1, st);
+        if (rc) return rc;
+        a.unscale = scale;
+        a.a = g;
+        a.pitch_a = plan.pitch_g();
+        if (c.want_dweight) {
+            a.b = hidden;
+            a.pitch_b = plan.wide * T::ESZ;
+            a.granules = (uint32_t)(plan.wide * T::ESZ / 16);
+            a.pitch_out = c.width * T::ESZ;
+            a.ktiles = (uint32_t)(plan.padded / plan.KT);
+            rc = launch_by_rows<T, kDweight>(a, 0, c.width, false, 1, st);
+            if (rc) return rc;
+        }
+        if (c.want_dhidden) {
+            a.pitch_b = pitch_w;
+            a.granules = (uint32_t)(pitch_w / 16);
+            a.first_piece = first;
+            if (plan.sums) {
+                a.out = sums;
+                a.pitch_out = plan.wide * sizeof(float);
+                rc = launch_by_rows<T, kDsums>(a, c.tokens, c.width, true, plan.splits, st);
+            } else {
+                a.out = c.dhidden;
+                a.pitch_out = c.width * T::ESZ;
+                rc = launch_by_rows<T, kDhidden>(a, c.tokens, c.width, true, 1, st);
+            }
+            if (rc) return rc;
+        }
+        first = false;
+    }
+    if (!plan.sums) return VRC_OK;
+    const unsigned gx = (unsigned)((c.width + 1023) / 1024);
+    k_entropy_join<T><<<dim3(gx, (unsigned)(c.tokens < 32768 ? c.tokens : 32768)), 256, 0, st>>>(
+        (const float*)sums, (uint32_t)plan.splits, (uint32_t)c.tokens, (uint32_t)c.width, (uint32_t)plan.wide, scale, c.dhidden);
+    return check_launch();
+}
+
+}  // namespace
+}  // namespace vrc

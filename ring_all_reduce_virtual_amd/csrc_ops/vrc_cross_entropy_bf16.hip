@@ -1,0 +1,15 @@
+// vrc_cross_entropy_bf16.hip -- the cross entropy's kernels of one element type.
+#include "vrc_cross_entropy.hpp"
+
+namespace vrc {
+namespace host {
+
+template <>
+uint64_t entropy_bytes<BF16>(const EntropyCall& c, bool gradient) { return EntropyPlan<BF16>(c, gradient).bytes; }
+template <>
+vrc_status_t entropy_loss<BF16>(const EntropyCall& c, hipStream_t st) { return cross_entropy_typed<BF16>(c, st); }
+template <>
+vrc_status_t entropy_grad<BF16>(const EntropyCall& c, hipStream_t st) { return cross_entropy_grad_typed<BF16>(c, st); }
+
+}  // namespace host
+}  // namespace vrc

@@ -18,7 +18,7 @@ from . import (MAX_RANKS, PKG, VRC_BF16, VRC_FP16, VRC_FP32, VRC_OK, VrcError, _
                reduce_scatter_shape)
 
 OPS_LIB_PATH = os.path.join(PKG, "libvrc_ops.so")
-OPS_VERSION = 100  # VRC_OPS_VERSION of include/vrc_ops.h that this binding follows
+OPS_VERSION = 101  # VRC_OPS_VERSION of include/vrc_ops.h that this binding follows
 MX4_BLOCK = 32     # values that share a scale
 MX4_ALONG_COLS, MX4_ALONG_ROWS = 0, 1
 MX4_JOINS = {"sum": 0, "each": 1}
