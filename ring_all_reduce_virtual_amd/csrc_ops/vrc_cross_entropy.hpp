@@ -136,8 +136,8 @@ __device__ __forceinline__ float exp_of(float x)
 
 // A workgroup of WM x WN waves has a BM x BN tile of the result, a wave MI x NI
 // matrix-instruction tiles of it.  A ring of S stages, up to S - 1 tiles of the
-// contraction ahead; one barrier a tile, behind which its loads have landed for
-// every wave and the stage of the tile before it is free.  Past the last tile the
+// contraction ahead; one barrier a tile, between its last read and its last step, behind
+// which the next tile has landed for every wave and this tile's stage is free.  Past the last tile the
 // loop goes on fetching that tile again, so that every wave always has the same number of
 // loads under way, which is what its waits count.
 // CUT: B's elements past the end of the contraction are read from a constant zero
@@ -225,29 +225,52 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
 
     f32x16 acc[MI][NI] = {};
     const uint32_t wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN), r = lane & 31, half = lane >> 5;
+    // A step's operands, one ahead of the matrix instructions.  The scheduling barriers
+    // keep the reads of a step in front of the instructions of the step before it: left
+    // alone, the compiler reads each operand right before its use and waits for it.
+    u32x4 x[2][MI], y[2][NI];
+    const auto settle = [] { __builtin_amdgcn_sched_barrier(0); };
+    const auto read = [&](const char* stage, int s) {
+#pragma unroll
+        for (int j = 0; j < NI; j++) y[s & 1][j] = B::read(stage + A::BYTES, wn + j * 32, s, lane);
+#pragma unroll
+        for (int i = 0; i < MI; i++) x[s & 1][i] = A::read(stage, wm + i * 32, s, lane);
+        settle();
+    };
+    const auto step = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < MI; i++)
+#pragma unroll
+            for (int j = 0; j < NI; j++) acc[i][j] = tile_mfma<T>(y[s & 1][j], x[s & 1][i], acc[i][j]);
+        settle();
+    };
     if (total) {
 #pragma unroll
-        for (int t = 0; t + 1 < S; t++) fetch();
+        for (int t = 0; t < S; t++) fetch();
+        wait_vmem_below<LOADS*(S - 1)>();
+        tile_barrier();
         uint32_t cur = 0;
-        for (uint32_t t = 0; t < total; t++) {
+        read(ring[0], 0);
+        const auto first_steps = [&] {
+            read(ring[cur], 1);
+            step(0);
+            read(ring[cur], 2);
+            step(1);
+            read(ring[cur], 3);
+            step(2);
+        };
+        for (uint32_t t = 1; t < total; t++) {
+            first_steps();
+            // the next tile has landed, for every wave behind the barrier, and this one's stage is free
             wait_vmem_below<LOADS*(S - 2)>();
             tile_barrier();
             fetch();
-            const char* stage = ring[cur];
             cur = cur + 1 == S ? 0 : cur + 1;
-#pragma unroll
-            for (int s = 0; s < 4; s++) {
-                u32x4 x[MI], y[NI];
-#pragma unroll
-                for (int j = 0; j < NI; j++) y[j] = B::read(stage + A::BYTES, wn + j * 32, s, lane);
-#pragma unroll
-                for (int i = 0; i < MI; i++) x[i] = A::read(stage, wm + i * 32, s, lane);
-#pragma unroll
-                for (int i = 0; i < MI; i++)
-#pragma unroll
-                    for (int j = 0; j < NI; j++) acc[i][j] = tile_mfma<T>(y[j], x[i], acc[i][j]);
-            }
+            read(ring[cur], 0);
+            step(3);
         }
+        first_steps();
+        step(3);
         wait_vmem_below<0>();
     }
     __syncthreads();
@@ -308,10 +331,12 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
             static_assert(WAVES * PART * T::ESZ <= S * STAGE, "the results' way out fits the ring");
             const uint32_t cols = a.piece[p].len - n0;
             Coef c[MI];
+            bool live[MI];
 #pragma unroll
             for (int i = 0; i < MI; i++) {
                 const uint32_t token = m0 + wm + i * 32 + r;
                 c[i] = a.coef[token < a.rows_a ? token : a.rows_a - 1];
+                live[i] = (c[i].a != 0.0f) | (c[i].b != 0.0f);  // NaN too
                 c[i].target -= a.piece[p].first + n0 + wn;
             }
             drain<T, MI, NI>(&ring[0][0] + wave * PART * T::ESZ, lane,
@@ -319,7 +344,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
                     const uint32_t col = j * 32 + result_col(e, half);
                     float g = c[i].a * exp_of<T>(acc[i][j][e] - c[i].lse);
                     g = col == c[i].target ? g - c[i].b : g;
-                    return (c[i].a == 0.0f && c[i].b == 0.0f) || wn + col >= cols ? 0.0f : g;
+                    return (live[i] & (wn + col < cols)) ? g : 0.0f;
                 },
                 [&](uint32_t row, uint32_t col, u32x4 x) {
                     const uint32_t token = m0 + wm + row;
@@ -360,12 +385,10 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
 // What stands around the products.
 // ---------------------------------------------------------------------------
 
-// A sum over a workgroup of 256, in every lane.
 __device__ __forceinline__ float group_max(float v, float* lds)
 {
 #pragma unroll
     for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
-    __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     v = lds[0];
@@ -373,43 +396,39 @@ __device__ __forceinline__ float group_max(float v, float* lds)
     return v;
 }
 
-__device__ __forceinline__ float group_sum(float v, float* lds)
+// (maximum, sum of exponentials of the differences from it) of two sets together.  A
+// maximum that is infinite takes differences from 0 instead, whose exponentials are 0 and
+// infinity; NaN stays in the sum.
+__device__ __forceinline__ float2 join_sums(float2 p, float2 q)
 {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m, 64);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
-    for (uint32_t w = 1; w < blockDim.x / 64; w++) v += lds[w];
-    return v;
+    const float top = fmaxf(p.x, q.x), from = __builtin_isinf(top) ? 0.0f : top;
+    return make_float2(top, p.y * expf(p.x - from) + q.y * expf(q.x - from));
 }
 
-// The tiles' maxima and sums of one token, joined by TOKENS lanes' columns: 256 lanes
-// are 16 tokens by 16 runs of tiles (neighbouring lanes read neighbouring tokens).
+// The tiles' maxima and sums of each token, joined: RUNS lanes have a token, whose tiles
+// they take in turn.  16 lanes, so that neighbouring ones read neighbouring tokens;
+// where tokens are few 256, as a lane's tiles follow one another at memory's latency (one
+// token's 512 tiles: 17 us with 16 lanes, 4 us with 256).
+template <int RUNS>
 __global__ __launch_bounds__(256) void k_entropy_loss(const float2* stats, const float* picked, uint32_t tiles, uint32_t tokens,
                                                       const long long* target, long long ignore, uint32_t vocab, float* loss,
                                                       float* lse)
 {
-    __shared__ float2 part[16][17];
-    const uint32_t c = threadIdx.x % 16, run = threadIdx.x / 16, token = blockIdx.x * 16 + c;
-    float top = -INFINITY, sum = 0.0f;
-    if (token < tokens) {
-        for (uint32_t i = run; i < tiles; i += 16) top = fmaxf(top, stats[(uint64_t)i * tokens + token].x);
-        const float from = __builtin_isinf(top) ? 0.0f : top;
-        for (uint32_t i = run; i < tiles; i += 16) {
-            const float2 v = stats[(uint64_t)i * tokens + token];
-            sum += v.y * expf(v.x - from);
-        }
-    }
-    part[run][c] = make_float2(top, sum);
+    constexpr uint32_t TOKENS = 256 / RUNS;
+    __shared__ float2 part[RUNS][TOKENS + 1];
+    const uint32_t c = threadIdx.x % TOKENS, run = threadIdx.x / TOKENS, token = blockIdx.x * TOKENS + c;
+    float2 s = make_float2(-INFINITY, 0.0f);
+    if (token < tokens)
+        for (uint32_t i = run; i < tiles; i += RUNS) s = join_sums(s, stats[(uint64_t)i * tokens + token]);
+    part[run][c] = s;
     __syncthreads();
+    for (uint32_t half = RUNS / 2; half; half /= 2) {
+        if (run < half) part[run][c] = join_sums(part[run][c], part[run + half][c]);
+        __syncthreads();
+    }
     if (run || token >= tokens) return;
-    for (int q = 1; q < 16; q++) top = fmaxf(top, part[q][c].x);
-    const float from = __builtin_isinf(top) ? 0.0f : top;
-    sum = 0.0f;
-    for (int q = 0; q < 16; q++) sum += part[q][c].y * expf(part[q][c].x - from);
-    const float l = from + logf(sum);
+    s = part[0][c];
+    const float l = (__builtin_isinf(s.x) ? 0.0f : s.x) + logf(s.y);
     lse[token] = l;
     if (!loss) return;
     const long long t = target[token];
@@ -591,10 +610,10 @@ struct EntropyPlan {
         if (pack_weight) at_weight = take(piece * wide * T::ESZ);
         at_g = take(padded * pitch_g());
         if (c.want_dhidden) {
-            // few tiles: the contraction is split until there are about two a CU
+            // few tiles: the contraction is split until each CU has one (256 x 256) or two
             const uint64_t bm = c.tokens <= 32 ? 32 : c.tokens <= 64 ? 64 : c.tokens <= 128 ? 128 : 256, bn = bm == 256 ? 256 : 128;
             const uint64_t tiles = ((c.tokens + bm - 1) / bm) * ((c.width + bn - 1) / bn);
-            uint64_t s = tiles >= kCus * 3 / 4 ? 1 : (2 * kCus + tiles - 1) / tiles;
+            uint64_t s = (bm == 256 ? kCus : 2 * kCus) / tiles;
             const uint64_t most = piece / KT / 4;  // of four tiles at least
             s = s < most ? s : most;
             splits = s < 1 ? 1 : s > 128 ? 128 : (int)s;
@@ -759,9 +778,15 @@ vrc_status_t cross_entropy_typed(const EntropyCall& c, hipStream_t st)
             if (rc) return rc;
             tiles += a.tiles_n;
         }
-        k_entropy_loss<<<(unsigned)((tokens + 15) / 16), 256, 0, st>>>(stats, picked, (uint32_t)tiles, (uint32_t)tokens,
-                                                                       c.loss ? c.target + t0 : nullptr, c.ignore_index,
-                                                                       (uint32_t)plan.vocab, c.loss ? c.loss + t0 : nullptr, c.lse + t0);
+        const long long* const target = c.loss ? c.target + t0 : nullptr;
+        float* const loss = c.loss ? c.loss + t0 : nullptr;
+        if (tokens <= 1024)
+            k_entropy_loss<256><<<(unsigned)tokens, 256, 0, st>>>(stats, picked, (uint32_t)tiles, (uint32_t)tokens, target,
+                                                                  c.ignore_index, (uint32_t)plan.vocab, loss, c.lse + t0);
+        else
+            k_entropy_loss<16><<<(unsigned)((tokens + 15) / 16), 256, 0, st>>>(stats, picked, (uint32_t)tiles, (uint32_t)tokens,
+                                                                               target, c.ignore_index, (uint32_t)plan.vocab, loss,
+                                                                               c.lse + t0);
         const vrc_status_t rc = check_launch();
         if (rc) return rc;
     }

@@ -358,20 +358,32 @@ __global__ __launch_bounds__(block_of(LANES)) void k_layer_norm_grad(NormArgs a)
 }
 
 // Column sums of the partial sums: out[k][col] = sum over p of partial[p][k][col],
-// k = 0 (dweight), 1 (dbias), in the order of p within each of 16 interleaved runs
-// and then of the runs.
+// k = 0 (dweight), 1 (dbias), in the order of p within each of 32 interleaved runs
+// and then of the runs.  Eight loads of a lane are under way at once.
 template <class T>
 __global__ __launch_bounds__(1024) void k_norm_join(const float* partial, uint32_t count, uint32_t width, char* dw, char* db)
 {
-    __shared__ float part[16][64];
-    const uint32_t c = threadIdx.x % 64, run = threadIdx.x / 64, col = blockIdx.x * 64 + c, k = blockIdx.y;
+    __shared__ float part[32][33];
+    const uint32_t c = threadIdx.x % 32, run = threadIdx.x / 32, col = blockIdx.x * 32 + c, k = blockIdx.y;
     float s = 0.0f;
-    if (col < width)
-        for (uint32_t p = run; p < count; p += 16) s += partial[((uint64_t)p * 2 + k) * width + col];
+    if (col < width) {
+        const float* from = partial + (uint64_t)k * width + col;
+        const uint64_t pitch = 2 * (uint64_t)width;
+        uint32_t p = run;
+        for (; p + 7 * 32 < count; p += 8 * 32) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = from[(p + i * 32) * pitch];
+            issue_loads_first();
+#pragma unroll
+            for (int i = 0; i < 8; i++) s += v[i];
+        }
+        for (; p < count; p += 32) s += from[p * pitch];
+    }
     part[run][c] = s;
     __syncthreads();
     if (run || col >= width) return;
-    for (int q = 1; q < 16; q++) s += part[q][c];
+    for (int q = 1; q < 32; q++) s += part[q][c];
     store_s<T>((k ? db : dw) + (uint64_t)col * T::ESZ, T::narrow(s));
 }
 
@@ -594,7 +606,7 @@ vrc_status_t norm_grad_typed(const NormCall& c, hipStream_t st)
         const vrc_status_t rc = norm_grad_rows<T>(c, a, groups, st);
         if (rc) return rc;
     }
-    const dim3 grid((unsigned)((c.width + 63) / 64), c.dbias ? 2 : 1);
+    const dim3 grid((unsigned)((c.width + 31) / 32), c.dbias ? 2 : 1);
     const uint32_t count = groups * (unsigned)c.parts;
     if (c.wide_weight) k_norm_join<F32><<<grid, 1024, 0, st>>>(c.partial, count, a.width, c.dweight, c.dbias);
     else k_norm_join<T><<<grid, 1024, 0, st>>>(c.partial, count, a.width, c.dweight, c.dbias);
