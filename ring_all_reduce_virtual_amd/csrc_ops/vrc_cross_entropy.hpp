@@ -13,6 +13,12 @@
 //            there are few tiles) in fp32.
 // G is the only thing kept, [tokens, a piece's columns]; DHIDDEN reads it along its
 // rows, DWEIGHT across them.
+//
+// Few tokens (kFewTokens at most) are a stream of the weights and one of their gradients.
+// There G is held as its transpose, a row of the weights' vocabulary a row, from which
+// k_entropy_dweight_few's operands come straight into registers; and, of 16-bit types, as
+// two values each, G rounded and what that left: the matrix cores have the time, and the
+// rounding of a few large elements of G would not average out as it does over many tokens.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -25,7 +31,8 @@ namespace {
 
 using host::EntropyCall;
 
-enum EntropyOp { kStats, kGrad, kDweight, kDhidden, kDsums };  // the last: DHIDDEN's sums, in fp32
+// kDsums: DHIDDEN's sums, in fp32.  kGradT and kDsumsT: of few tokens, by G's transpose.
+enum EntropyOp { kStats, kGrad, kGradT, kDweight, kDhidden, kDsums, kDsumsT };
 
 // A run of one rank's weight rows.
 struct Piece {
@@ -116,7 +123,7 @@ template <class T>
 __device__ __forceinline__ void store_some(char* to, u32x4 x, uint32_t left)
 {
     if (left >= T::VEC) {
-        st16<false>(to, x);
+        st16<true>(to, x);
         return;
     }
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -146,9 +153,9 @@ template <class T, int OP, int BM, int BN, int WM, int WN, int S, bool CUT>
 __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
 {
     constexpr int MI = BM / WM / 32, NI = BN / WN / 32, WAVES = WM * WN;
-    constexpr bool DHIDDEN = OP == kDhidden || OP == kDsums;
-    typedef TileOperand<T, OP == kDweight ? kAcross : kAlong, BM> A;
-    typedef TileOperand<T, OP == kStats || OP == kGrad ? kAlong : kAcross, BN> B;
+    constexpr bool DHIDDEN = OP == kDhidden || OP == kDsums || OP == kDsumsT, LOGITS = OP == kStats || OP == kGrad || OP == kGradT;
+    typedef TileOperand<T, OP == kDweight || OP == kDsumsT ? kAcross : kAlong, BM> A;
+    typedef TileOperand<T, LOGITS ? kAlong : kAcross, BN> B;
     constexpr uint32_t LOADS = (A::LOADS + B::LOADS) / WAVES, STAGE = A::BYTES + B::BYTES, KT = kTileK<T>;
     static_assert((A::LOADS + B::LOADS) % WAVES == 0 && S >= 2 && LOADS * (S - 1) < 64, "loads are shared out evenly");
     __shared__ __attribute__((aligned(16))) char ring[S][STAGE];
@@ -181,11 +188,11 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
         const uint32_t at = wave * LOADS + i;
         if (at < A::LOADS) {
             // across: a piece's columns of G are there up to a multiple of 256
-            const uint32_t last = OP == kDweight ? 0xffffffffu : a.rows_a - 1 - m0;
+            const uint32_t last = OP == kDweight || OP == kDsumsT ? 0xffffffffu : a.rows_a - 1 - m0;
             A::source(at * 64 + lane, (uint32_t)a.pitch_a, last, off[i], kk[i]);
             kk[i] = 0;
         } else {
-            const uint32_t last = OP == kStats || OP == kGrad ? a.piece[p].len - 1 - n0 : a.granules - 1 - n0 * T::ESZ / 16;
+            const uint32_t last = LOGITS ? a.piece[p].len - 1 - n0 : a.granules - 1 - n0 * T::ESZ / 16;
             B::source((at - A::LOADS) * 64 + lane, (uint32_t)a.pitch_b, last, off[i], kk[i]);
         }
     }
@@ -196,7 +203,8 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
         if constexpr (DHIDDEN) {
             const Piece& q = a.piece[p];
             const uint32_t k = (kt - q.tile) * KT;
-            pa = a.a + m0 * a.pitch_a + (uint64_t)(q.col + k) * T::ESZ;
+            if constexpr (OP == kDsumsT) pa = a.a + (uint64_t)(q.col + k) * a.pitch_a + (uint64_t)m0 * T::ESZ;
+            else pa = a.a + m0 * a.pitch_a + (uint64_t)(q.col + k) * T::ESZ;
             pb = q.w + (uint64_t)k * a.pitch_b + (uint64_t)n0 * T::ESZ;
             left = q.len - k;
         } else if constexpr (OP == kDweight) {
@@ -241,7 +249,8 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
 #pragma unroll
         for (int i = 0; i < MI; i++)
 #pragma unroll
-            for (int j = 0; j < NI; j++) acc[i][j] = tile_mfma<T>(y[s & 1][j], x[s & 1][i], acc[i][j]);
+            for (int j = 0; j < NI; j++)  // G's transpose: rows of it to lanes
+                acc[i][j] = OP == kGradT ? tile_mfma<T>(x[s & 1][i], y[s & 1][j], acc[i][j]) : tile_mfma<T>(y[s & 1][j], x[s & 1][i], acc[i][j]);
         settle();
     };
     if (total) {
@@ -326,7 +335,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
             a.stats[(uint64_t)tn * a.tokens + m0 + m] = make_float2(top, sum);
         }
     } else {
-        constexpr uint32_t PART = 32 * NI * 32;  // results of a wave on their way out
+        [[maybe_unused]] constexpr uint32_t PART = 32 * NI * 32;  // results of a wave on their way out
         if constexpr (OP == kGrad) {
             static_assert(WAVES * PART * T::ESZ <= S * STAGE, "the results' way out fits the ring");
             const uint32_t cols = a.piece[p].len - n0;
@@ -350,7 +359,40 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
                     const uint32_t token = m0 + wm + row;
                     if (token < a.rows_a) st16<false>(a.out + token * a.pitch_out + (uint64_t)(a.piece[p].col + n0 + wn + col) * T::ESZ, x);
                 });
-        } else if constexpr (OP == kDsums) {
+        } else if constexpr (OP == kGradT) {
+            // a lane has a row of the transpose, four consecutive tokens at a time
+            const uint32_t cols = a.piece[p].len - n0;
+#pragma unroll
+            for (int i = 0; i < MI; i++)
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    const uint32_t token = m0 + wm + i * 32 + result_col(4 * g, half);
+                    Coef c[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) c[e] = a.coef[token + e];
+#pragma unroll
+                    for (int j = 0; j < NI; j++) {
+                        const uint32_t col = wn + j * 32 + r, v = a.piece[p].first + n0 + col;
+                        float hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            float x = c[e].a * exp_of<T>(acc[i][j][4 * g + e] - c[e].lse);
+                            x = v == c[e].target ? x - c[e].b : x;
+                            hi[e] = (((c[e].a != 0.0f) | (c[e].b != 0.0f)) & (col < cols)) ? x : 0.0f;
+                            const float kept = T::widen(T::narrow(hi[e]));
+                            lo[e] = __builtin_isfinite(kept) ? hi[e] - kept : 0.0f;
+                        }
+                        char* const to = a.out + (uint64_t)(a.piece[p].col + n0 + col) * a.pitch_out + token * T::ESZ;
+                        const Quad<T> h(hi), l(lo);
+                        if constexpr (T::ESZ == 4) {
+                            *(u32x4*)to = u32x4{h.w[0], h.w[1], h.w[2], h.w[3]};
+                        } else {
+                            *(u32x2*)to = u32x2{h.w[0], h.w[1]};
+                            *(u32x2*)(to + a.rows_a * T::ESZ) = u32x2{l.w[0], l.w[1]};
+                        }
+                    }
+                }
+        } else if constexpr (OP == kDsums || OP == kDsumsT) {
             static_assert(WAVES * PART * 4 <= S * STAGE, "the results' way out fits the ring");
             char* const out = a.out + blockIdx.y * (uint64_t)a.tokens * a.pitch_out;
             drain<F32, MI, NI>(&ring[0][0] + wave * PART * 4, lane, [&](int i, int j, int e) { return acc[i][j][e]; },
@@ -378,6 +420,62 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
                     if (m < rows && n < a.width) store_some<T>(out + m * a.pitch_out + (uint64_t)n * T::ESZ, x, a.width - n);
                 });
         }
+    }
+}
+
+// DWEIGHT of few tokens: a stream of stores.  A wave keeps the hidden states of its NI x
+// 32 columns in registers and walks a run of the vocabulary, 32 rows at a time, whose
+// rows of G's transpose (`steps` granules a lane, the next 32 rows' under way while these
+// are multiplied) are its other operand.  Neighbouring waves have neighbouring columns
+// of the same rows, so that lines of a row are written at about the same time.
+// a.b: the hidden states' transpose, [columns, STEPS * 2 granules].
+template <class T, int STEPS, int NI>
+__global__ __launch_bounds__(512) void k_entropy_dweight_few(EntropyArgs a, uint32_t waves)
+{
+    constexpr int PARTS = T::ESZ == 2 ? 2 : 1;
+    constexpr uint32_t PART = 32 * NI * 32;
+    __shared__ __attribute__((aligned(16))) char out[8][PART * T::ESZ];
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r = lane & 31, half = lane >> 5, id = blockIdx.x * 8 + wave;
+    if (id >= waves) return;  // no barrier follows
+    const uint32_t groups = a.tiles_n, runs = waves / groups, run = id / groups, n0 = id % groups * (NI * 32);
+    const uint32_t t0 = (uint32_t)(a.ktiles * (uint64_t)run / runs), t1 = (uint32_t)(a.ktiles * (uint64_t)(run + 1) / runs);
+    if (t0 >= t1) return;
+    u32x4 y[STEPS][NI];
+#pragma unroll
+    for (int j = 0; j < NI; j++) {
+        const uint32_t col = n0 + j * 32 + r;
+        const char* from = a.b + (col < a.width ? col : a.width - 1) * a.pitch_b + half * 16;
+#pragma unroll
+        for (int s = 0; s < STEPS; s++) y[s][j] = ld16<false>(from + s * 32);
+    }
+    int p = 0;
+    while (p + 1 < a.pieces && t0 >= a.piece[p + 1].tile) p++;
+    const float u = *a.unscale;
+    u32x4 x[PARTS * STEPS];
+    const auto fetch = [&](uint32_t t, int q) {  // rows past a piece's end are zero or those of a multiple of 256, and not stored
+        const char* from = a.a + (uint64_t)(a.piece[q].col + (t - a.piece[q].tile) * 32 + r) * a.pitch_a + half * 16;
+#pragma unroll
+        for (int s = 0; s < PARTS * STEPS; s++) x[s] = ld16<false>(from + s * 32);
+    };
+    fetch(t0, p);
+    for (uint32_t t = t0; t < t1; t++) {
+        f32x16 acc[1][NI] = {};
+#pragma unroll
+        for (int s = 0; s < PARTS * STEPS; s++)
+#pragma unroll
+            for (int j = 0; j < NI; j++) acc[0][j] = tile_mfma<T>(y[s % STEPS][j], x[s], acc[0][j]);
+        const uint32_t v0 = (t - a.piece[p].tile) * 32, rows = a.piece[p].len;
+        char* const to = a.piece[p].out;
+        if (t + 1 < t1) {
+            p += p + 1 < a.pieces && t + 1 >= a.piece[p + 1].tile;
+            fetch(t + 1, p);
+        }
+        drain<T, 1, NI>(out[wave], lane, [&](int i, int j, int e) { return acc[i][j][e] * u; },
+            [&](uint32_t row, uint32_t col, u32x4 v) {
+                const uint32_t n = n0 + col;
+                if (v0 + row < rows && n < a.width) store_some<T>(to + (v0 + row) * a.pitch_out + (uint64_t)n * T::ESZ, v, a.width - n);
+            });
     }
 }
 
@@ -514,19 +612,38 @@ __global__ __launch_bounds__(256) void k_entropy_pack(const char* src, char* dst
     }
 }
 
-// out = unscale x the splits' sums, in their order, rounded.
+// The transpose of the packed hidden states of few tokens: [width][padded].
 template <class T>
-__global__ __launch_bounds__(256) void k_entropy_join(const float* sums, uint32_t splits, uint32_t tokens, uint32_t width,
-                                                      uint32_t pitch, const float* unscale, char* out)
+__global__ __launch_bounds__(256) void k_entropy_transpose(const char* src, char* dst, uint32_t padded, uint32_t width, uint32_t granules)
+{
+    const uint32_t col = blockIdx.x * 256 + threadIdx.x, g = blockIdx.y;
+    if (col >= width) return;
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < T::VEC; e++) {
+        const uint32_t s = load_s<T>(src + (uint64_t)(g * T::VEC + e) * granules * 16 + (uint64_t)col * T::ESZ);
+        if constexpr (T::ESZ == 4) w[e] = s;
+        else w[e / 2] |= s << (16 * (e & 1));
+    }
+    st16<false>(dst + ((uint64_t)col * padded * T::ESZ + g * 16), u32x4{w[0], w[1], w[2], w[3]});
+}
+
+// out = unscale x the sums of every split and, in it, of every part (few tokens: of G
+// rounded and of what that left), in their order, rounded.
+template <class T>
+__global__ __launch_bounds__(256) void k_entropy_join(const float* sums, uint32_t splits, uint32_t parts, uint32_t rows,
+                                                      uint32_t tokens, uint32_t width, uint32_t pitch, const float* unscale,
+                                                      char* out)
 {
     const float u = *unscale;
     const uint32_t quads = (width + 3) / 4;
     for (uint32_t row = blockIdx.y; row < tokens; row += gridDim.y)
         for (uint32_t q = blockIdx.x * 256 + threadIdx.x; q < quads; q += gridDim.x * 256) {
             float s[4] = {};
-            for (uint32_t i = 0; i < splits; i++) {
+#pragma unroll 4
+            for (uint32_t i = 0; i < splits * parts; i++) {
                 float v[4];
-                F32::unpack(ld16<false>((const char*)(sums + ((uint64_t)i * tokens + row) * pitch + q * 4)), v);
+                F32::unpack(ld16<false>((const char*)(sums + ((uint64_t)i * rows + row) * pitch + q * 4)), v);
 #pragma unroll
                 for (int e = 0; e < 4; e++) s[e] += v[e];
             }
@@ -549,6 +666,7 @@ __global__ __launch_bounds__(256) void k_entropy_zero(char* out, uint64_t count)
 using namespace host;
 
 constexpr uint64_t kCus = 256;               // of the card this library is built for; plans do not ask the device
+constexpr uint64_t kFewTokens = 128;
 constexpr uint64_t kPieceBytes = 128u << 20; // G of one piece of the vocabulary, and packed weights: half the last-level cache
 
 inline uint64_t up_to(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
@@ -558,6 +676,8 @@ inline uint64_t up_to(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 template <class T>
 struct EntropyPlan {
     static constexpr uint64_t KT = kTileK<T>;
+    bool few = false;
+    uint64_t parts = 1, rows = 0;     // of G's elements (few tokens); rows of DHIDDEN's sums, parts of `padded` each
     uint64_t vocab = 0, columns = 0;  // the whole; the same with each rank's rounded up to 256
     uint64_t padded, wide;            // tokens rounded up to 64; elements of a packed row
     bool pack_hidden, pack_weight, cut;
@@ -565,7 +685,7 @@ struct EntropyPlan {
     uint64_t tokens;                  // of one pass (the loss)
     int splits = 1;                   // of DHIDDEN's contraction
     bool sums = false;                // whether DHIDDEN goes by fp32 sums
-    uint64_t at_hidden = 0, at_weight = 0, at_stats = 0, at_picked = 0, at_coef = 0, at_scale = 0, at_g = 0, at_sums = 0, bytes = 0;
+    uint64_t at_hidden = 0, at_transpose = 0, at_weight = 0, at_stats = 0, at_picked = 0, at_coef = 0, at_scale = 0, at_g = 0, at_sums = 0, bytes = 0;
 
     uint64_t take(uint64_t size)
     {
@@ -585,7 +705,10 @@ struct EntropyPlan {
             if (c.vocab[r]) pack_weight |= !direct(c.width, (uintptr_t)c.weight[r]);
         }
         wide = up_to(c.width, KT);
-        padded = up_to(c.tokens ? c.tokens : 1, 64);
+        few = gradient && c.tokens <= kFewTokens;
+        padded = few ? (c.tokens <= 32 ? 32 : c.tokens <= 64 ? 64 : 128) : up_to(c.tokens ? c.tokens : 1, 64);
+        parts = few && T::ESZ == 2 ? 2 : 1;
+        rows = few ? parts * padded : c.tokens;
         cut = c.width % KT != 0 && !pack_weight;
         // the gradient's hidden states are always packed: rows of tokens without gradient are zero
         pack_hidden = gradient ? true : c.width % KT != 0 || !direct(c.width, (uintptr_t)c.hidden);
@@ -602,23 +725,24 @@ struct EntropyPlan {
         }
         if (columns == 0) return;
         // pieces of a few thousand columns at least, so that the sums over them cost little
-        piece = limit(piece, kPieceBytes / (padded * T::ESZ), 4096);
+        piece = limit(piece, kPieceBytes / (padded * parts * T::ESZ), 4096);
         piece = up_to((columns + pieces_of(piece) - 1) / pieces_of(piece), 256);  // of about one size
         at_coef = take(padded * sizeof(Coef));
         at_scale = take(16);
         at_hidden = take(padded * wide * T::ESZ);
         if (pack_weight) at_weight = take(piece * wide * T::ESZ);
-        at_g = take(padded * pitch_g());
+        if (few && c.want_dweight) at_transpose = take(c.width * padded * T::ESZ);
+        at_g = take(few ? piece * pitch_gt() : padded * pitch_g());
         if (c.want_dhidden) {
             // few tiles: the contraction is split until each CU has one (256 x 256) or two
-            const uint64_t bm = c.tokens <= 32 ? 32 : c.tokens <= 64 ? 64 : c.tokens <= 128 ? 128 : 256, bn = bm == 256 ? 256 : 128;
-            const uint64_t tiles = ((c.tokens + bm - 1) / bm) * ((c.width + bn - 1) / bn);
+            const uint64_t bm = few ? rows : 256, bn = bm == 256 ? 256 : 128;
+            const uint64_t tiles = ((rows + bm - 1) / bm) * ((c.width + bn - 1) / bn);
             uint64_t s = (bm == 256 ? kCus : 2 * kCus) / tiles;
             const uint64_t most = piece / KT / 4;  // of four tiles at least
             s = s < most ? s : most;
             splits = s < 1 ? 1 : s > 128 ? 128 : (int)s;
-            sums = splits > 1 || pieces_of(piece) > 1;
-            if (sums) at_sums = take((uint64_t)splits * c.tokens * wide * sizeof(float));
+            sums = few || splits > 1 || pieces_of(piece) > 1;
+            if (sums) at_sums = take((uint64_t)splits * rows * wide * sizeof(float));
         }
     }
     // At most `most` columns (rounded down to 256), but no fewer than `least`.
@@ -630,6 +754,9 @@ struct EntropyPlan {
     }
     // A row of G: 128 bytes more than its columns, so that rows start on other memory channels.
     uint64_t pitch_g() const { return piece * T::ESZ + 128; }
+    // Rows from one part of the sums to the next.
+    uint64_t padded_rows() const { return few ? padded : rows; }
+    uint64_t pitch_gt() const { return padded * parts * T::ESZ; }
 };
 
 // The pieces of the vocabulary, a few at a time: `columns` of them at most.
@@ -673,7 +800,7 @@ vrc_status_t launch_entropy(EntropyArgs& a, uint64_t rows, uint64_t cols, bool c
 {
     a.tiles_m = (uint32_t)((rows + BM - 1) / BM);
     a.tiles_n = (uint32_t)((cols + BN - 1) / BN);
-    constexpr bool DHIDDEN = OP == kDhidden || OP == kDsums;
+    constexpr bool DHIDDEN = OP == kDhidden || OP == kDsums || OP == kDsumsT;
     if constexpr (DHIDDEN) {
         uint32_t t = 0;
         for (int i = 0; i < a.pieces; i++) {
@@ -704,18 +831,46 @@ vrc_status_t launch_entropy(EntropyArgs& a, uint64_t rows, uint64_t cols, bool c
     return check_launch();
 }
 
-// Tiles by the rows of the result (tokens; for DWEIGHT the vocabulary's).
+// Tiles by the rows of the result.  Up to kFewTokens one tile has all tokens, and the
+// others are as small as keeps two workgroups' rings in a CU's LDS.
 template <class T, int OP>
 vrc_status_t launch_by_rows(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut, int splits, hipStream_t st)
 {
-    if constexpr (OP != kDweight) {
-        if (a.tokens <= 32) return launch_entropy<T, OP, 32, 128, 1, 4, 4>(a, rows, cols, cut, splits, st);
-        if (a.tokens <= 64) return launch_entropy<T, OP, 64, 128, 1, 4, 3>(a, rows, cols, cut, splits, st);
-        if (a.tokens <= 128) return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
-    } else {
-        if (a.tokens <= 128) return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
+    if constexpr (OP == kStats || OP == kGradT || OP == kDsumsT) {
+        if (rows <= 32) return launch_entropy<T, OP, 32, 128, 1, 4, 4>(a, rows, cols, cut, splits, st);
+        if (rows <= 64) return launch_entropy<T, OP, 64, 128, 1, 4, 3>(a, rows, cols, cut, splits, st);
+        if (rows <= 128) return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
     }
-    return launch_entropy<T, OP, 256, 256, 2, 4, 2>(a, rows, cols, cut, splits, st);
+    if constexpr (OP == kGradT || (OP == kDsumsT && T::ESZ == 4)) return VRC_ERR_INVALID_ARG;
+    else return launch_entropy<T, OP, 256, 256, 2, 4, 2>(a, rows, cols, cut, splits, st);
+}
+
+template <class T, int STEPS, int NI>
+vrc_status_t launch_dweight_few(EntropyArgs& a, hipStream_t st)
+{
+    uint32_t t = 0;
+    for (int i = 0; i < a.pieces; i++) {
+        a.piece[i].tile = t;
+        t += (a.piece[i].len + 31) / 32;
+    }
+    a.ktiles = t;
+    a.tiles_n = (a.width + NI * 32 - 1) / (NI * 32);
+    // two workgroups of eight waves a CU, but runs of four times 32 rows at least
+    uint64_t runs = (2 * 8 * kCus + a.tiles_n - 1) / a.tiles_n;
+    const uint64_t most = (t + 3) / 4;
+    runs = runs < most ? runs : most;
+    const uint64_t waves = runs * a.tiles_n;
+    k_entropy_dweight_few<T, STEPS, NI><<<(unsigned)((waves + 7) / 8), 512, 0, st>>>(a, (uint32_t)waves);
+    return check_launch();
+}
+
+template <class T>
+vrc_status_t dweight_few(EntropyArgs& a, uint64_t padded, hipStream_t st)
+{
+    constexpr int S = T::ESZ;  // steps of 32 bytes: 16 tokens of 16 bits, 8 of 32
+    if (padded == 32) return launch_dweight_few<T, S, T::ESZ == 2 ? 4 : 2>(a, st);
+    if (padded == 64) return launch_dweight_few<T, 2 * S, T::ESZ == 2 ? 4 : 2>(a, st);
+    return launch_dweight_few<T, 4 * S, 2>(a, st);
 }
 
 template <class T>
@@ -817,6 +972,13 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
     rc = pack<T>(c.hidden, hidden, c.tokens, plan.padded, c.width, plan.wide, coef, st);
     if (rc) return rc;
 
+    if (plan.few && c.want_dweight) {
+        k_entropy_transpose<T><<<dim3((unsigned)((c.width + 255) / 256), (unsigned)(plan.padded / T::VEC)), 256, 0, st>>>(
+            hidden, c.workspace + plan.at_transpose, (uint32_t)plan.padded, (uint32_t)c.width, (uint32_t)(plan.wide * T::ESZ / 16));
+        rc = check_launch();
+        if (rc) return rc;
+    }
+
     EntropyArgs a = {};
     PieceWalk walk = {c, plan.piece};
     bool first = true;
@@ -837,21 +999,13 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
         a.ktiles = (uint32_t)(plan.wide / plan.KT);
         a.coef = coef;
         a.out = g;
-        a.pitch_out = plan.pitch_g();
-        rc = launch_by_rows<T, kGrad>(a, plan.padded, 0, plan.cut, 1, st);
+        a.pitch_out = plan.few ? plan.pitch_gt() : plan.pitch_g();
+        rc = plan.few ? launch_by_rows<T, kGradT>(a, plan.padded, 0, plan.cut, 1, st)
+                      : launch_by_rows<T, kGrad>(a, plan.padded, 0, plan.cut, 1, st);
         if (rc) return rc;
         a.unscale = scale;
         a.a = g;
-        a.pitch_a = plan.pitch_g();
-        if (c.want_dweight) {
-            a.b = hidden;
-            a.pitch_b = plan.wide * T::ESZ;
-            a.granules = (uint32_t)(plan.wide * T::ESZ / 16);
-            a.pitch_out = c.width * T::ESZ;
-            a.ktiles = (uint32_t)(plan.padded / plan.KT);
-            rc = launch_by_rows<T, kDweight>(a, 0, c.width, false, 1, st);
-            if (rc) return rc;
-        }
+        a.pitch_a = a.pitch_out;
         if (c.want_dhidden) {
             a.pitch_b = pitch_w;
             a.granules = (uint32_t)(pitch_w / 16);
@@ -859,11 +1013,28 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
             if (plan.sums) {
                 a.out = sums;
                 a.pitch_out = plan.wide * sizeof(float);
-                rc = launch_by_rows<T, kDsums>(a, c.tokens, c.width, true, plan.splits, st);
+                a.tokens = (uint32_t)plan.rows;
+                rc = plan.few ? launch_by_rows<T, kDsumsT>(a, plan.rows, c.width, true, plan.splits, st)
+                              : launch_by_rows<T, kDsums>(a, plan.rows, c.width, true, plan.splits, st);
             } else {
                 a.out = c.dhidden;
                 a.pitch_out = c.width * T::ESZ;
                 rc = launch_by_rows<T, kDhidden>(a, c.tokens, c.width, true, 1, st);
+            }
+            if (rc) return rc;
+        }
+        if (c.want_dweight) {
+            a.pitch_out = c.width * T::ESZ;
+            if (plan.few) {
+                a.b = c.workspace + plan.at_transpose;
+                a.pitch_b = plan.padded * T::ESZ;
+                rc = dweight_few<T>(a, plan.padded, st);
+            } else {
+                a.b = hidden;
+                a.pitch_b = plan.wide * T::ESZ;
+                a.granules = (uint32_t)(plan.wide * T::ESZ / 16);
+                a.ktiles = (uint32_t)(plan.padded / plan.KT);
+                rc = launch_by_rows<T, kDweight>(a, 0, c.width, false, 1, st);
             }
             if (rc) return rc;
         }
@@ -872,7 +1043,7 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
     if (!plan.sums) return VRC_OK;
     const unsigned gx = (unsigned)((c.width + 1023) / 1024);
     k_entropy_join<T><<<dim3(gx, (unsigned)(c.tokens < 32768 ? c.tokens : 32768)), 256, 0, st>>>(
-        (const float*)sums, (uint32_t)plan.splits, (uint32_t)c.tokens, (uint32_t)c.width, (uint32_t)plan.wide, scale, c.dhidden);
+        (const float*)sums, (uint32_t)plan.splits, (uint32_t)plan.parts, (uint32_t)plan.padded_rows(), (uint32_t)c.tokens, (uint32_t)c.width, (uint32_t)plan.wide, scale, c.dhidden);
     return check_launch();
 }
 

@@ -362,6 +362,7 @@ vrc_status_t vrc_cross_entropy_grad_workspace(const vrc_cross_entropy_t* ce, con
     const vrc_status_t rc = entropy_call(ce, hidden, weight, nranks, &c, &dt);
     if (rc) return rc;
     c.want_dhidden = dhidden != 0 && c.tokens;
+    c.want_dweight = true;
     *bytes = workspace_of(c, dt, true);
     return VRC_OK;
 }
