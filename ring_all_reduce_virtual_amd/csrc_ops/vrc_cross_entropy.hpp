@@ -580,18 +580,25 @@ __global__ __launch_bounds__(1024) void k_entropy_coef(const long long* target, 
     if (threadIdx.x == 0) scale[0] = unit;
 }
 
-// Rows of a matrix at a pitch of whole tiles, zero behind each row's end, behind the
-// last row and (where coef is given) in rows of tokens without gradient: what those hold
-// then reaches no product.
+// Matrices of one width, and how many rows of each there are and are written.
+struct PackArgs {
+    const char* src[kMaxRanks];
+    char* dst[kMaxRanks];
+    uint32_t rows[kMaxRanks], padded[kMaxRanks];
+};
+
+// Rows at a pitch of whole tiles, zero behind each row's end, behind the last row and
+// (where coef is given) in rows of tokens without gradient: what those hold then
+// reaches no product.  `lanes` (a power of two up to 256) have a row.
 template <class T>
-__global__ __launch_bounds__(256) void k_entropy_pack(const char* src, char* dst, uint32_t rows, uint32_t padded, uint32_t width,
-                                                      uint32_t granules, const Coef* coef)
+__global__ __launch_bounds__(256) void k_entropy_pack(PackArgs a, uint32_t width, uint32_t granules, uint32_t lanes, const Coef* coef)
 {
-    for (uint32_t row = blockIdx.x; row < padded; row += gridDim.x) {
-        bool live = row < rows;
+    const uint32_t m = blockIdx.y, per = 256 / lanes, lane = threadIdx.x & (lanes - 1);
+    for (uint32_t row = blockIdx.x * per + threadIdx.x / lanes; row < a.padded[m]; row += gridDim.x * per) {
+        bool live = row < a.rows[m];
         if (live && coef) live = coef[row].a != 0.0f || coef[row].b != 0.0f;
-        const char* from = src + (uint64_t)row * width * T::ESZ;
-        for (uint32_t g = threadIdx.x; g < granules; g += 256) {
+        const char* from = a.src[m] + (uint64_t)row * width * T::ESZ;
+        for (uint32_t g = lane; g < granules; g += lanes) {
             const uint32_t col = g * T::VEC;
             u32x4 x = {0, 0, 0, 0};
             if (live && col < width) {
@@ -599,7 +606,9 @@ __global__ __launch_bounds__(256) void k_entropy_pack(const char* src, char* dst
                     x = ld16<false>(from + (uint64_t)g * 16);
                 } else {
                     uint32_t w[4] = {0, 0, 0, 0};
-                    for (uint32_t e = 0; col + e < width; e++) {
+#pragma unroll
+                    for (uint32_t e = 0; e < T::VEC; e++) {
+                        if (col + e >= width) continue;
                         const uint32_t s = load_s<T>(from + (uint64_t)(col + e) * T::ESZ);
                         if constexpr (T::ESZ == 4) w[e] = s;
                         else w[e / 2] |= s << (16 * (e & 1));
@@ -607,7 +616,7 @@ __global__ __launch_bounds__(256) void k_entropy_pack(const char* src, char* dst
                     x = u32x4{w[0], w[1], w[2], w[3]};
                 }
             }
-            st16<false>(dst + ((uint64_t)row * granules + g) * 16, x);
+            st16<false>(a.dst[m] + ((uint64_t)row * granules + g) * 16, x);
         }
     }
 }
@@ -667,7 +676,8 @@ using namespace host;
 
 constexpr uint64_t kCus = 256;               // of the card this library is built for; plans do not ask the device
 constexpr uint64_t kFewTokens = 128;
-constexpr uint64_t kPieceBytes = 128u << 20; // G of one piece of the vocabulary, and packed weights: half the last-level cache
+constexpr uint64_t kPieceBytes = 128u << 20; // G of one piece of the vocabulary: half the last-level cache
+constexpr uint64_t kPackBytes = 1u << 30;    // packed weights of one piece: enough tiles for all CUs
 
 inline uint64_t up_to(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
@@ -683,7 +693,7 @@ struct EntropyPlan {
     bool pack_hidden, pack_weight, cut;
     uint64_t piece;                   // columns of a piece at most, a multiple of 256
     uint64_t tokens;                  // of one pass (the loss)
-    int splits = 1;                   // of DHIDDEN's contraction
+    int side = 0, splits = 1;         // of DHIDDEN: of a tile; of its contraction
     bool sums = false;                // whether DHIDDEN goes by fp32 sums
     uint64_t at_hidden = 0, at_transpose = 0, at_weight = 0, at_stats = 0, at_picked = 0, at_coef = 0, at_scale = 0, at_g = 0, at_sums = 0, bytes = 0;
 
@@ -713,13 +723,13 @@ struct EntropyPlan {
         // the gradient's hidden states are always packed: rows of tokens without gradient are zero
         pack_hidden = gradient ? true : c.width % KT != 0 || !direct(c.width, (uintptr_t)c.hidden);
         piece = up_to(columns, 256);
-        if (pack_weight) piece = limit(piece, kPieceBytes / (wide * T::ESZ), 256);
+        if (pack_weight) piece = limit(piece, kPackBytes / (wide * T::ESZ), 256);
         tokens = c.tokens;
         if (!gradient) {
             tokens = c.tokens < 16384 ? c.tokens : 16384;
             if (pack_hidden) at_hidden = take(c.tokens * wide * T::ESZ);
             if (pack_weight) at_weight = take(piece * wide * T::ESZ);
-            at_stats = take((columns / 128) * tokens * sizeof(float2));
+            at_stats = take((columns / 64) * tokens * sizeof(float2));
             at_picked = take(tokens * sizeof(float));
             return;
         }
@@ -734,11 +744,13 @@ struct EntropyPlan {
         if (few && c.want_dweight) at_transpose = take(c.width * padded * T::ESZ);
         at_g = take(few ? piece * pitch_gt() : padded * pitch_g());
         if (c.want_dhidden) {
-            // few tiles: the contraction is split until each CU has one (256 x 256) or two
-            const uint64_t bm = few ? rows : 256, bn = bm == 256 ? 256 : 128;
-            const uint64_t tiles = ((rows + bm - 1) / bm) * ((c.width + bn - 1) / bn);
-            uint64_t s = (bm == 256 ? kCus : 2 * kCus) / tiles;
-            const uint64_t most = piece / KT / 4;  // of four tiles at least
+            // Few tiles: the contraction is split until each CU has one (256 x 256) or two,
+            // of four tiles at least.
+            const auto tiles = [&](uint64_t bm, uint64_t bn) { return ((rows + bm - 1) / bm) * ((c.width + bn - 1) / bn); };
+            if (!few) side = T::ESZ == 2 && tiles(256, 256) >= kCus / 2 ? 256 : tiles(128, 128) > 8 ? 128 : 64;
+            const uint64_t bm = few ? rows : side, bn = few ? (rows == 256 ? 256 : 128) : side;
+            uint64_t s = (bm == 256 ? kCus : 2 * kCus) / tiles(bm, bn);
+            const uint64_t most = piece / KT / 4;
             s = s < most ? s : most;
             splits = s < 1 ? 1 : s > 128 ? 128 : (int)s;
             sums = few || splits > 1 || pieces_of(piece) > 1;
@@ -831,18 +843,54 @@ vrc_status_t launch_entropy(EntropyArgs& a, uint64_t rows, uint64_t cols, bool c
     return check_launch();
 }
 
-// Tiles by the rows of the result.  Up to kFewTokens one tile has all tokens, and the
-// others are as small as keeps two workgroups' rings in a CU's LDS.
-template <class T, int OP>
-vrc_status_t launch_by_rows(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut, int splits, hipStream_t st)
+// Tiles of b x b in a product of rows x cols, whose vocabulary side (if any) is in pieces.
+template <int OP>
+uint64_t tiles_of(const EntropyArgs& a, uint64_t rows, uint64_t cols, uint64_t b)
 {
-    if constexpr (OP == kStats || OP == kGradT || OP == kDsumsT) {
-        if (rows <= 32) return launch_entropy<T, OP, 32, 128, 1, 4, 4>(a, rows, cols, cut, splits, st);
-        if (rows <= 64) return launch_entropy<T, OP, 64, 128, 1, 4, 3>(a, rows, cols, cut, splits, st);
-        if (rows <= 128) return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
-    }
-    if constexpr (OP == kGradT || (OP == kDsumsT && T::ESZ == 4)) return VRC_ERR_INVALID_ARG;
-    else return launch_entropy<T, OP, 256, 256, 2, 4, 2>(a, rows, cols, cut, splits, st);
+    uint64_t along = 0;
+    for (int i = 0; i < a.pieces; i++) along += (a.piece[i].len + b - 1) / b;
+    if constexpr (OP == kStats || OP == kGrad) return (rows + b - 1) / b * along;
+    else if constexpr (OP == kDweight) return (cols + b - 1) / b * along;
+    else return ((rows + b - 1) / b) * ((cols + b - 1) / b);
+}
+
+// The tile's side of a product of `tiles(b)` tiles of b x b: the smallest of which two a CU
+// are enough.  fp32's matrix instructions take so long that tiles of 128 feed them as well
+// as larger ones.
+template <class T, class Tiles>
+int tile_side(Tiles tiles)
+{
+    if (tiles(64) <= 2 * kCus) return 64;
+    return T::ESZ == 4 || tiles(128) <= 2 * kCus ? 128 : 256;
+}
+
+// The product, by tiles of one side.
+template <class T, int OP>
+vrc_status_t launch_side(EntropyArgs& a, int side, uint64_t rows, uint64_t cols, bool cut, int splits, hipStream_t st)
+{
+    if (side == 64) return launch_entropy<T, OP, 64, 64, 2, 2, 4>(a, rows, cols, cut, splits, st);
+    if constexpr (T::ESZ == 2)
+        if (side == 256) return launch_entropy<T, OP, 256, 256, 2, 4, 2>(a, rows, cols, cut, splits, st);
+    return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
+}
+
+template <class T, int OP>
+vrc_status_t launch_tiles(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut, hipStream_t st)
+{
+    const int side = tile_side<T>([&](uint64_t b) { return tiles_of<OP>(a, rows, cols, b); });
+    return launch_side<T, OP>(a, side, rows, cols, cut, 1, st);
+}
+
+// Few rows (tokens): one tile has all of them, and its other side is as small as keeps two
+// workgroups' rings in a CU's LDS.
+template <class T, int OP>
+vrc_status_t launch_few(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut, int splits, hipStream_t st)
+{
+    if (rows <= 32) return launch_entropy<T, OP, 32, 128, 1, 4, 4>(a, rows, cols, cut, splits, st);
+    if (rows <= 64) return launch_entropy<T, OP, 64, 128, 1, 4, 3>(a, rows, cols, cut, splits, st);
+    if constexpr (OP == kDsumsT && T::ESZ == 2)
+        if (rows > 128) return launch_entropy<T, OP, 256, 256, 2, 4, 2>(a, rows, cols, cut, splits, st);
+    return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
 }
 
 template <class T, int STEPS, int NI>
@@ -874,13 +922,27 @@ vrc_status_t dweight_few(EntropyArgs& a, uint64_t padded, hipStream_t st)
 }
 
 template <class T>
-vrc_status_t pack(const char* src, char* dst, uint64_t rows, uint64_t padded, uint64_t width, uint64_t wide, const Coef* coef,
-                  hipStream_t st)
+vrc_status_t pack(const PackArgs& p, int count, uint64_t width, uint64_t wide, const Coef* coef, hipStream_t st)
 {
-    if (padded == 0) return VRC_OK;
-    k_entropy_pack<T><<<(unsigned)(padded < 65536 ? padded : 65536), 256, 0, st>>>(src, dst, (uint32_t)rows, (uint32_t)padded, (uint32_t)width,
-                                                                              (uint32_t)(wide * T::ESZ / 16), coef);
+    const uint32_t granules = (uint32_t)(wide * T::ESZ / 16);
+    uint32_t lanes = 8, most = 0;
+    while (lanes < 256 && lanes < granules) lanes *= 2;
+    for (int i = 0; i < count; i++) most = p.padded[i] > most ? p.padded[i] : most;
+    const uint32_t groups = most / (256 / lanes) + 1;
+    k_entropy_pack<T><<<dim3(groups < 65536 ? groups : 65536, (unsigned)count), 256, 0, st>>>(p, (uint32_t)width, granules, lanes, coef);
     return check_launch();
+}
+
+template <class T>
+vrc_status_t pack_one(const char* src, char* dst, uint64_t rows, uint64_t padded, uint64_t width, uint64_t wide, const Coef* coef,
+                      hipStream_t st)
+{
+    PackArgs p = {};
+    p.src[0] = src;
+    p.dst[0] = dst;
+    p.rows[0] = (uint32_t)rows;
+    p.padded[0] = (uint32_t)padded;
+    return pack<T>(p, 1, width, wide, coef, st);
 }
 
 // The launch's pieces in the packed form.
@@ -888,13 +950,15 @@ template <class T>
 vrc_status_t pack_pieces(const EntropyCall& c, const EntropyPlan<T>& plan, EntropyArgs& a, hipStream_t st)
 {
     char* to = c.workspace + plan.at_weight;
+    PackArgs p = {};
     for (int i = 0; i < a.pieces; i++) {
-        const vrc_status_t rc = pack<T>(a.piece[i].w, to, a.piece[i].len, a.piece[i].len, c.width, plan.wide, nullptr, st);
-        if (rc) return rc;
+        p.src[i] = a.piece[i].w;
+        p.dst[i] = to;
+        p.rows[i] = p.padded[i] = a.piece[i].len;
         a.piece[i].w = to;
         to += (uint64_t)a.piece[i].len * plan.wide * T::ESZ;
     }
-    return VRC_OK;
+    return pack<T>(p, a.pieces, c.width, plan.wide, nullptr, st);
 }
 
 template <class T>
@@ -904,7 +968,7 @@ vrc_status_t cross_entropy_typed(const EntropyCall& c, hipStream_t st)
     const char* hidden = c.hidden;
     if (plan.pack_hidden) {
         char* const to = c.workspace + plan.at_hidden;
-        const vrc_status_t rc = pack<T>(c.hidden, to, c.tokens, c.tokens, c.width, plan.wide, nullptr, st);
+        const vrc_status_t rc = pack_one<T>(c.hidden, to, c.tokens, c.tokens, c.width, plan.wide, nullptr, st);
         if (rc) return rc;
         hidden = to;
     }
@@ -929,7 +993,8 @@ vrc_status_t cross_entropy_typed(const EntropyCall& c, hipStream_t st)
             a.tokens = a.rows_a = (uint32_t)tokens;
             a.kwidth = (uint32_t)c.width;
             a.ktiles = (uint32_t)(plan.wide / plan.KT);
-            const vrc_status_t rc = launch_by_rows<T, kStats>(a, tokens, 0, plan.cut, 1, st);
+            const vrc_status_t rc = tokens <= 64 ? launch_few<T, kStats>(a, tokens, 0, plan.cut, 1, st)
+                                                 : launch_tiles<T, kStats>(a, tokens, 0, plan.cut, st);
             if (rc) return rc;
             tiles += a.tiles_n;
         }
@@ -969,7 +1034,7 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
                                           (uint32_t)c.tokens, (uint32_t)plan.padded, coef, scale);
     vrc_status_t rc = check_launch();
     if (rc) return rc;
-    rc = pack<T>(c.hidden, hidden, c.tokens, plan.padded, c.width, plan.wide, coef, st);
+    rc = pack_one<T>(c.hidden, hidden, c.tokens, plan.padded, c.width, plan.wide, coef, st);
     if (rc) return rc;
 
     if (plan.few && c.want_dweight) {
@@ -1000,8 +1065,8 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
         a.coef = coef;
         a.out = g;
         a.pitch_out = plan.few ? plan.pitch_gt() : plan.pitch_g();
-        rc = plan.few ? launch_by_rows<T, kGradT>(a, plan.padded, 0, plan.cut, 1, st)
-                      : launch_by_rows<T, kGrad>(a, plan.padded, 0, plan.cut, 1, st);
+        rc = plan.few ? launch_few<T, kGradT>(a, plan.padded, 0, plan.cut, 1, st)
+                      : launch_tiles<T, kGrad>(a, plan.padded, 0, plan.cut, st);
         if (rc) return rc;
         a.unscale = scale;
         a.a = g;
@@ -1014,12 +1079,12 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
                 a.out = sums;
                 a.pitch_out = plan.wide * sizeof(float);
                 a.tokens = (uint32_t)plan.rows;
-                rc = plan.few ? launch_by_rows<T, kDsumsT>(a, plan.rows, c.width, true, plan.splits, st)
-                              : launch_by_rows<T, kDsums>(a, plan.rows, c.width, true, plan.splits, st);
+                rc = plan.few ? launch_few<T, kDsumsT>(a, plan.rows, c.width, true, plan.splits, st)
+                              : launch_side<T, kDsums>(a, plan.side, plan.rows, c.width, true, plan.splits, st);
             } else {
                 a.out = c.dhidden;
                 a.pitch_out = c.width * T::ESZ;
-                rc = launch_by_rows<T, kDhidden>(a, c.tokens, c.width, true, 1, st);
+                rc = launch_side<T, kDhidden>(a, plan.side, c.tokens, c.width, true, 1, st);
             }
             if (rc) return rc;
         }
@@ -1034,7 +1099,7 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
                 a.pitch_b = plan.wide * T::ESZ;
                 a.granules = (uint32_t)(plan.wide * T::ESZ / 16);
                 a.ktiles = (uint32_t)(plan.padded / plan.KT);
-                rc = launch_by_rows<T, kDweight>(a, 0, c.width, false, 1, st);
+                rc = launch_tiles<T, kDweight>(a, 0, c.width, false, st);
             }
             if (rc) return rc;
         }
