@@ -1,6 +1,8 @@
-"""Build the HIP libraries (libvrc.so, libvrc_ops.so) for gfx950 with hipcc, in-tree."""
+"""Build the HIP libraries (libvrc.so, libvrc_ops.so) for gfx950 with hipcc, in-tree,
+and the compiled Python binding of the model's operators (_vrc_model.so) with g++."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
@@ -75,9 +77,34 @@ def build_cvt_check(verbose: bool = False) -> str:
     return CVT_CHECK_BIN
 
 
+BINDING_SRC = os.path.join(CSRC_OPS, "vrc_model_binding.cpp")
+BINDING_LIB = os.path.join(PKG, "_vrc_model.so")
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Build the compiled Python binding of include/vrc_model.h against torch's
+    headers and libvrc_ops.so (host code only)."""
+    import sysconfig
+
+    spec = importlib.util.find_spec("torch")
+    torch = os.path.dirname(spec.origin)
+    tmp = BINDING_LIB + ".tmp"
+    system = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-Wno-attributes", "-DUSE_ROCM",
+           "-D__HIP_PLATFORM_AMD__=1", *(a for d in system for a in ("-isystem", d)), "-I", INCLUDE, "-o", tmp, BINDING_SRC,
+           "-L", PKG, "-l:libvrc_ops.so", "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING_LIB)
+    return BINDING_LIB
+
+
 def build(verbose: bool = False, jobs: int = 0) -> str:
     """Compile every source to an object (in parallel), link libvrc.so and
-    libvrc_ops.so, and return libvrc.so's path."""
+    libvrc_ops.so and the binding on it, and return libvrc.so's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     sources = SOURCES + SOURCES_OPS
     jobs = jobs or min(len(sources), os.cpu_count() or 1, 16)
@@ -107,6 +134,7 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, lib)
+    build_binding(verbose)
     return LIB
 
 

@@ -747,7 +747,7 @@ struct EntropyPlan {
             // Few tiles: the contraction is split until each CU has one (256 x 256) or two,
             // of four tiles at least.
             const auto tiles = [&](uint64_t bm, uint64_t bn) { return ((rows + bm - 1) / bm) * ((c.width + bn - 1) / bn); };
-            if (!few) side = T::ESZ == 2 && tiles(256, 256) >= kCus / 2 ? 256 : tiles(128, 128) > 8 ? 128 : 64;
+            if (!few) side = T::ESZ == 2 && tiles(256, 256) > 8 ? 256 : tiles(128, 128) > 8 ? 128 : 64;
             const uint64_t bm = few ? rows : side, bn = few ? (rows == 256 ? 256 : 128) : side;
             uint64_t s = (bm == 256 ? kCus : 2 * kCus) / tiles(bm, bn);
             const uint64_t most = piece / KT / 4;
