@@ -147,8 +147,8 @@ __device__ __forceinline__ float exp_of(float x)
 // which the next tile has landed for every wave and this tile's stage is free.  Past the last tile the
 // loop goes on fetching that tile again, so that every wave always has the same number of
 // loads under way, which is what its waits count.
-// CUT: B's elements past the end of the contraction are read from a constant zero
-// (A's are zero in memory, or are multiplied by those).
+// CUT (LOGITS): B's elements past the end of a row are read from a constant zero (A's
+// are zero in memory).
 template <class T, int OP, int BM, int BN, int WM, int WN, int S, bool CUT>
 __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
 {
@@ -196,10 +196,11 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
             B::source((at - A::LOADS) * 64 + lane, (uint32_t)a.pitch_b, last, off[i], kk[i]);
         }
     }
-    uint32_t kt = t0, fetched = 0, fstage = 0;  // kt: of the tile that is fetched next
-    const auto fetch = [&] {
-        const char *pa, *pb;
-        uint32_t left = ~0u;
+    // The tile that is fetched next, and where it lies: found while the one before it is
+    // multiplied, so that behind the barrier its loads go out at once.
+    uint32_t kt = t0, fetched = 0, fstage = 0, left = ~0u;
+    const char *pa = nullptr, *pb = nullptr;
+    const auto aim = [&] {
         if constexpr (DHIDDEN) {
             const Piece& q = a.piece[p];
             const uint32_t k = (kt - q.tile) * KT;
@@ -215,20 +216,30 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
             pb = a.piece[p].w + n0 * a.pitch_b + (uint64_t)kt * kTileRow;
             left = a.kwidth - kt * KT;
         }
-#pragma unroll
-        for (uint32_t i = 0; i < LOADS; i++) {
-            const uint32_t at = wave * LOADS + i;
-            auto from = (global_ptr<const char>)(at < A::LOADS ? pa : pb) + hidden_offset(off[i]);
-            if constexpr (CUT)
-                if (kk[i] >= left) from = (global_ptr<const char>)&kZeroGranule;
-            granules_to_lds(from, ring[fstage] + at * 1024);
-        }
+    };
+    const auto load = [&](uint32_t i) {
+        const uint32_t at = wave * LOADS + i;
+        uint32_t o = off[i];
+        if constexpr (DHIDDEN)  // rows of the weights past a piece's end, times G's zeros: its last row again
+            o -= kk[i] < left ? 0 : (kk[i] - left + 1) * (uint32_t)a.pitch_b;
+        auto from = (global_ptr<const char>)(at < A::LOADS ? pa : pb) + hidden_offset(o);
+        if constexpr (CUT && !DHIDDEN)
+            if (kk[i] >= left) from = (global_ptr<const char>)&kZeroGranule;
+        granules_to_lds(from, ring[fstage] + at * 1024);
+    };
+    const auto advance = [&] {
         fstage = fstage + 1 == S ? 0 : fstage + 1;
         fetched++;
         if (fetched < total) {
             kt++;
             if constexpr (DHIDDEN) p += p + 1 < a.pieces && kt >= a.piece[p + 1].tile;
         }
+    };
+    const auto fetch = [&] {
+        aim();
+#pragma unroll
+        for (uint32_t i = 0; i < LOADS; i++) load(i);
+        advance();
     };
 
     f32x16 acc[MI][NI] = {};
@@ -245,12 +256,14 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
         for (int i = 0; i < MI; i++) x[s & 1][i] = A::read(stage, wm + i * 32, s, lane);
         settle();
     };
+    const auto multiply = [&](int s, int i) {
+#pragma unroll
+        for (int j = 0; j < NI; j++)  // G's transpose: rows of it to lanes
+            acc[i][j] = OP == kGradT ? tile_mfma<T>(x[s & 1][i], y[s & 1][j], acc[i][j]) : tile_mfma<T>(y[s & 1][j], x[s & 1][i], acc[i][j]);
+    };
     const auto step = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < MI; i++)
-#pragma unroll
-            for (int j = 0; j < NI; j++)  // G's transpose: rows of it to lanes
-                acc[i][j] = OP == kGradT ? tile_mfma<T>(x[s & 1][i], y[s & 1][j], acc[i][j]) : tile_mfma<T>(y[s & 1][j], x[s & 1][i], acc[i][j]);
+        for (int i = 0; i < MI; i++) multiply(s, i);
         settle();
     };
     if (total) {
@@ -269,14 +282,23 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
             step(2);
         };
         for (uint32_t t = 1; t < total; t++) {
+            aim();
             first_steps();
             // the next tile has landed, for every wave behind the barrier, and this one's stage is free
             wait_vmem_below<LOADS*(S - 2)>();
             tile_barrier();
-            fetch();
             cur = cur + 1 == S ? 0 : cur + 1;
             read(ring[cur], 0);
-            step(3);
+            // the loads between the matrix instructions of the last step
+#pragma unroll
+            for (int i = 0; i < MI; i++) {
+                multiply(3, i);
+                settle();
+#pragma unroll
+                for (uint32_t l = i * LOADS / MI; l < (i + 1) * LOADS / MI; l++) load(l);
+                settle();
+            }
+            advance();
         }
         first_steps();
         step(3);
@@ -835,7 +857,7 @@ vrc_status_t launch_entropy(EntropyArgs& a, uint64_t rows, uint64_t cols, bool c
     if constexpr (OP == kDweight) {
         k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
     } else if constexpr (DHIDDEN) {
-        k_entropy<T, OP, BM, BN, WM, WN, S, true><<<grid, WM * WN * 64, 0, st>>>(a);
+        k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
     } else {
         if (cut) k_entropy<T, OP, BM, BN, WM, WN, S, true><<<grid, WM * WN * 64, 0, st>>>(a);
         else k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
