@@ -555,32 +555,50 @@ __global__ __launch_bounds__(256) void k_entropy_loss(const float2* stats, const
     loss[token] = t == ignore ? 0.0f : (unsigned long long)t < vocab ? l - picked[token] : __builtin_nanf("");
 }
 
+// What the gradient's launches share of the call.
+struct TokenArgs {
+    const long long* target;
+    const float* lse;
+    const float* dloss;
+    const float* dlse;  // or null
+    long long ignore;
+    uint32_t vocab, tokens, padded;
+};
+
+__device__ __forceinline__ Coef coef_of(const TokenArgs& a, uint32_t t)
+{
+    const long long at = a.target[t];
+    const bool none = at == a.ignore, bad = !none && (unsigned long long)at >= a.vocab;
+    Coef c;
+    c.b = none ? 0.0f : a.dloss[t];
+    c.a = c.b + (a.dlse ? a.dlse[t] : 0.0f);
+    if (bad) c.a = __builtin_nanf("");
+    c.lse = a.lse[t];
+    c.target = none || bad ? kNoTarget : (uint32_t)at;
+    return c;
+}
+
+// Whether a token has any gradient; what the others' hidden states hold reaches nothing.
+__device__ __forceinline__ bool live(const TokenArgs& a, uint32_t t)
+{
+    if (t >= a.tokens) return false;
+    const Coef c = coef_of(a, t);
+    return c.a != 0.0f || c.b != 0.0f;
+}
+
 // The tokens' coefficients, by one workgroup.  16-bit G is held in units of the largest
 // |a| or |b| (fp16: 2^-14 of it): the targets' elements of a loss whose tokens weigh
 // the same are then rounded from 1 - p instead of from an arbitrary weight, and fp16's
 // small range does not matter.  scale[0]: one such unit.
 template <class T>
-__global__ __launch_bounds__(1024) void k_entropy_coef(const long long* target, const float* lse, const float* dloss,
-                                                       const float* dlse, long long ignore, uint32_t vocab, uint32_t tokens,
-                                                       uint32_t padded, Coef* coef, float* scale)
+__device__ __forceinline__ void write_coefs(const TokenArgs& a, Coef* coef, float* scale, float* lds)
 {
-    __shared__ float lds[16];
-    const auto of = [&](uint32_t t) {
-        const long long at = target[t];
-        const bool none = at == ignore, bad = !none && (unsigned long long)at >= vocab;
-        Coef c;
-        c.b = none ? 0.0f : dloss[t];
-        c.a = c.b + (dlse ? dlse[t] : 0.0f);
-        if (bad) c.a = __builtin_nanf("");
-        c.lse = lse[t];
-        c.target = none || bad ? kNoTarget : (uint32_t)at;
-        return c;
-    };
+    const uint32_t lanes = blockDim.x;
     float unit = 1.0f, up = 1.0f;
     if constexpr (T::ESZ == 2) {
         float most = 0.0f;
-        for (uint32_t t = threadIdx.x; t < tokens; t += 1024) {
-            const Coef c = of(t);
+        for (uint32_t t = threadIdx.x; t < a.tokens; t += lanes) {
+            const Coef c = coef_of(a, t);
             const float x = fmaxf(fabsf(c.a), fabsf(c.b));
             most = fmaxf(most, __builtin_isfinite(x) ? x : 0.0f);
         }
@@ -590,10 +608,10 @@ __global__ __launch_bounds__(1024) void k_entropy_coef(const long long* target, 
         unit = __is_same(T, F16) ? most * 0x1p-14f : most;
         up = 1.0f / unit;
     }
-    for (uint32_t t = threadIdx.x; t < padded; t += 1024) {
+    for (uint32_t t = threadIdx.x; t < a.padded; t += lanes) {
         Coef c = {0.0f, 0.0f, 0.0f, kNoTarget};
-        if (t < tokens) {
-            c = of(t);
+        if (t < a.tokens) {
+            c = coef_of(a, t);
             c.a *= up;
             c.b *= up;
         }
@@ -609,54 +627,77 @@ struct PackArgs {
     uint32_t rows[kMaxRanks], padded[kMaxRanks];
 };
 
-// Rows at a pitch of whole tiles, zero behind each row's end, behind the last row and
-// (where coef is given) in rows of tokens without gradient: what those hold then
-// reaches no product.  `lanes` (a power of two up to 256) have a row.
+// Granule g of a row of `width` elements, zero behind its end.
 template <class T>
-__global__ __launch_bounds__(256) void k_entropy_pack(PackArgs a, uint32_t width, uint32_t granules, uint32_t lanes, const Coef* coef)
+__device__ __forceinline__ u32x4 row_granule(const char* row, uint32_t g, uint32_t width)
+{
+    const uint32_t col = g * T::VEC;
+    if (col + T::VEC <= width) return ld16<false>(row + (uint64_t)g * 16);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (uint32_t e = 0; e < T::VEC; e++) {
+        if (col + e >= width) continue;
+        const uint32_t s = load_s<T>(row + (uint64_t)(col + e) * T::ESZ);
+        if constexpr (T::ESZ == 4) w[e] = s;
+        else w[e / 2] |= s << (16 * (e & 1));
+    }
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
+// Rows at a pitch of whole tiles, zero behind each row's end and behind the last row.
+// `lanes` (a power of two up to 256) have a row.
+template <class T>
+__global__ __launch_bounds__(256) void k_entropy_pack(PackArgs a, uint32_t width, uint32_t granules, uint32_t lanes)
 {
     const uint32_t m = blockIdx.y, per = 256 / lanes, lane = threadIdx.x & (lanes - 1);
     for (uint32_t row = blockIdx.x * per + threadIdx.x / lanes; row < a.padded[m]; row += gridDim.x * per) {
-        bool live = row < a.rows[m];
-        if (live && coef) live = coef[row].a != 0.0f || coef[row].b != 0.0f;
         const char* from = a.src[m] + (uint64_t)row * width * T::ESZ;
         for (uint32_t g = lane; g < granules; g += lanes) {
-            const uint32_t col = g * T::VEC;
             u32x4 x = {0, 0, 0, 0};
-            if (live && col < width) {
-                if (col + T::VEC <= width) {
-                    x = ld16<false>(from + (uint64_t)g * 16);
-                } else {
-                    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (uint32_t e = 0; e < T::VEC; e++) {
-                        if (col + e >= width) continue;
-                        const uint32_t s = load_s<T>(from + (uint64_t)(col + e) * T::ESZ);
-                        if constexpr (T::ESZ == 4) w[e] = s;
-                        else w[e / 2] |= s << (16 * (e & 1));
-                    }
-                    x = u32x4{w[0], w[1], w[2], w[3]};
-                }
-            }
+            if (row < a.rows[m]) x = row_granule<T>(from, g, width);
             st16<false>(a.dst[m] + ((uint64_t)row * granules + g) * 16, x);
         }
     }
 }
 
-// The transpose of the packed hidden states of few tokens: [width][padded].
+// What the gradient's products start from, in one launch.  blockIdx.y 0: the tokens'
+// coefficients (one workgroup); 1: the hidden states packed, rows of tokens without
+// gradient zero, so that what those hold reaches no product; 2 (few tokens): their
+// transpose, [width][padded].
 template <class T>
-__global__ __launch_bounds__(256) void k_entropy_transpose(const char* src, char* dst, uint32_t padded, uint32_t width, uint32_t granules)
+__global__ __launch_bounds__(256) void k_entropy_prepare(TokenArgs a, const char* hidden, uint32_t width, uint32_t granules,
+                                                         uint32_t lanes, char* packed, char* transpose, Coef* coef, float* scale)
 {
-    const uint32_t col = blockIdx.x * 256 + threadIdx.x, g = blockIdx.y;
-    if (col >= width) return;
-    uint32_t w[4] = {0, 0, 0, 0};
+    __shared__ float lds[4];
+    if (blockIdx.y == 0) {
+        if (blockIdx.x == 0) write_coefs<T>(a, coef, scale, lds);
+    } else if (blockIdx.y == 1) {
+        const uint32_t per = 256 / lanes, lane = threadIdx.x & (lanes - 1);
+        for (uint32_t row = blockIdx.x * per + threadIdx.x / lanes; row < a.padded; row += gridDim.x * per) {
+            const bool has = live(a, row);
+            const char* from = hidden + (uint64_t)row * width * T::ESZ;
+            for (uint32_t g = lane; g < granules; g += lanes) {
+                u32x4 x = {0, 0, 0, 0};
+                if (has) x = row_granule<T>(from, g, width);
+                st16<false>(packed + ((uint64_t)row * granules + g) * 16, x);
+            }
+        }
+    } else {
+        const uint32_t each = a.padded / T::VEC;  // granules of a column
+        const uint64_t count = (uint64_t)width * each;
+        for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < count; i += gridDim.x * 256ull) {
+            const uint32_t g = (uint32_t)(i / width), col = (uint32_t)(i - (uint64_t)g * width);
+            uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < T::VEC; e++) {
-        const uint32_t s = load_s<T>(src + (uint64_t)(g * T::VEC + e) * granules * 16 + (uint64_t)col * T::ESZ);
-        if constexpr (T::ESZ == 4) w[e] = s;
-        else w[e / 2] |= s << (16 * (e & 1));
+            for (uint32_t e = 0; e < T::VEC; e++) {
+                const uint32_t t = g * T::VEC + e;
+                const uint32_t s = live(a, t) ? load_s<T>(hidden + ((uint64_t)t * width + col) * T::ESZ) : 0;
+                if constexpr (T::ESZ == 4) w[e] = s;
+                else w[e / 2] |= s << (16 * (e & 1));
+            }
+            st16<false>(transpose + ((uint64_t)col * a.padded * T::ESZ + g * 16), u32x4{w[0], w[1], w[2], w[3]});
+        }
     }
-    st16<false>(dst + ((uint64_t)col * padded * T::ESZ + g * 16), u32x4{w[0], w[1], w[2], w[3]});
 }
 
 // out = unscale x the sums of every split and, in it, of every part (few tokens: of G
@@ -943,28 +984,23 @@ vrc_status_t dweight_few(EntropyArgs& a, uint64_t padded, hipStream_t st)
     return launch_dweight_few<T, 4 * S, 2>(a, st);
 }
 
-template <class T>
-vrc_status_t pack(const PackArgs& p, int count, uint64_t width, uint64_t wide, const Coef* coef, hipStream_t st)
+// Lanes for a row of granules.
+inline uint32_t row_lanes(uint32_t granules)
 {
-    const uint32_t granules = (uint32_t)(wide * T::ESZ / 16);
-    uint32_t lanes = 8, most = 0;
+    uint32_t lanes = 8;
     while (lanes < 256 && lanes < granules) lanes *= 2;
-    for (int i = 0; i < count; i++) most = p.padded[i] > most ? p.padded[i] : most;
-    const uint32_t groups = most / (256 / lanes) + 1;
-    k_entropy_pack<T><<<dim3(groups < 65536 ? groups : 65536, (unsigned)count), 256, 0, st>>>(p, (uint32_t)width, granules, lanes, coef);
-    return check_launch();
+    return lanes;
 }
 
 template <class T>
-vrc_status_t pack_one(const char* src, char* dst, uint64_t rows, uint64_t padded, uint64_t width, uint64_t wide, const Coef* coef,
-                      hipStream_t st)
+vrc_status_t pack(const PackArgs& p, int count, uint64_t width, uint64_t wide, hipStream_t st)
 {
-    PackArgs p = {};
-    p.src[0] = src;
-    p.dst[0] = dst;
-    p.rows[0] = (uint32_t)rows;
-    p.padded[0] = (uint32_t)padded;
-    return pack<T>(p, 1, width, wide, coef, st);
+    const uint32_t granules = (uint32_t)(wide * T::ESZ / 16), lanes = row_lanes(granules);
+    uint32_t most = 0;
+    for (int i = 0; i < count; i++) most = p.padded[i] > most ? p.padded[i] : most;
+    const uint32_t groups = most / (256 / lanes) + 1;
+    k_entropy_pack<T><<<dim3(groups < 65536 ? groups : 65536, (unsigned)count), 256, 0, st>>>(p, (uint32_t)width, granules, lanes);
+    return check_launch();
 }
 
 // The launch's pieces in the packed form.
@@ -980,7 +1016,7 @@ vrc_status_t pack_pieces(const EntropyCall& c, const EntropyPlan<T>& plan, Entro
         a.piece[i].w = to;
         to += (uint64_t)a.piece[i].len * plan.wide * T::ESZ;
     }
-    return pack<T>(p, a.pieces, c.width, plan.wide, nullptr, st);
+    return pack<T>(p, a.pieces, c.width, plan.wide, st);
 }
 
 template <class T>
@@ -990,7 +1026,11 @@ vrc_status_t cross_entropy_typed(const EntropyCall& c, hipStream_t st)
     const char* hidden = c.hidden;
     if (plan.pack_hidden) {
         char* const to = c.workspace + plan.at_hidden;
-        const vrc_status_t rc = pack_one<T>(c.hidden, to, c.tokens, c.tokens, c.width, plan.wide, nullptr, st);
+        PackArgs p = {};
+        p.src[0] = c.hidden;
+        p.dst[0] = to;
+        p.rows[0] = p.padded[0] = (uint32_t)c.tokens;
+        const vrc_status_t rc = pack<T>(p, 1, c.width, plan.wide, st);
         if (rc) return rc;
         hidden = to;
     }
@@ -1052,19 +1092,12 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
     char* const hidden = c.workspace + plan.at_hidden;
     char* const g = c.workspace + plan.at_g;
     char* const sums = c.workspace + plan.at_sums;
-    k_entropy_coef<T><<<1, 1024, 0, st>>>(c.target, c.lse, c.dloss, c.dlse, c.ignore_index, (uint32_t)plan.vocab,
-                                          (uint32_t)c.tokens, (uint32_t)plan.padded, coef, scale);
+    const TokenArgs tokens = {c.target, c.lse, c.dloss, c.dlse, c.ignore_index, (uint32_t)plan.vocab, (uint32_t)c.tokens, (uint32_t)plan.padded};
+    const uint32_t granules = (uint32_t)(plan.wide * T::ESZ / 16), lanes = row_lanes(granules), groups = (uint32_t)plan.padded / (256 / lanes) + 1;
+    k_entropy_prepare<T><<<dim3(groups < 65536 ? groups : 65536, plan.few && c.want_dweight ? 3 : 2), 256, 0, st>>>(
+        tokens, c.hidden, (uint32_t)c.width, granules, lanes, hidden, c.workspace + plan.at_transpose, coef, scale);
     vrc_status_t rc = check_launch();
     if (rc) return rc;
-    rc = pack_one<T>(c.hidden, hidden, c.tokens, plan.padded, c.width, plan.wide, coef, st);
-    if (rc) return rc;
-
-    if (plan.few && c.want_dweight) {
-        k_entropy_transpose<T><<<dim3((unsigned)((c.width + 255) / 256), (unsigned)(plan.padded / T::VEC)), 256, 0, st>>>(
-            hidden, c.workspace + plan.at_transpose, (uint32_t)plan.padded, (uint32_t)c.width, (uint32_t)(plan.wide * T::ESZ / 16));
-        rc = check_launch();
-        if (rc) return rc;
-    }
 
     EntropyArgs a = {};
     PieceWalk walk = {c, plan.piece};
