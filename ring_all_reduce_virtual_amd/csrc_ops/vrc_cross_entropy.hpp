@@ -14,11 +14,11 @@
 // G is the only thing kept, [tokens, a piece's columns]; DHIDDEN reads it along its
 // rows, DWEIGHT across them.
 //
-// Few tokens (kFewTokens at most) are a stream of the weights and one of their gradients.
-// There G is held as its transpose, a row of the weights' vocabulary a row, from which
-// k_entropy_dweight_few's operands come straight into registers; and, of 16-bit types, as
+// Few tokens (kFewTokens at most) are bound by the weights' bytes and their gradients'.
+// There G is held as its transpose, a row of the vocabulary a row, and, of 16-bit types, as
 // two values each, G rounded and what that left: the matrix cores have the time, and the
-// rounding of a few large elements of G would not average out as it does over many tokens.
+// rounding of a few large elements of G does not average out as it does over many tokens
+// (7 tokens: errors of the weights' gradients 0.0028 of their norm, bf16's own rounding 0.0017).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -31,8 +31,8 @@ namespace {
 
 using host::EntropyCall;
 
-// kDsums: DHIDDEN's sums, in fp32.  kGradT and kDsumsT: of few tokens, by G's transpose.
-enum EntropyOp { kStats, kGrad, kGradT, kDweight, kDhidden, kDsums, kDsumsT };
+// kDsums: DHIDDEN's sums, in fp32.  kGradT, kDweightT and kDsumsT: of few tokens, by G's transpose.
+enum EntropyOp { kStats, kGrad, kGradT, kDweight, kDweightT, kDhidden, kDsums, kDsumsT };
 
 // A run of one rank's weight rows.
 struct Piece {
@@ -154,6 +154,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
 {
     constexpr int MI = BM / WM / 32, NI = BN / WN / 32, WAVES = WM * WN;
     constexpr bool DHIDDEN = OP == kDhidden || OP == kDsums || OP == kDsumsT, LOGITS = OP == kStats || OP == kGrad || OP == kGradT;
+    constexpr bool DWEIGHT = OP == kDweight || OP == kDweightT;
     typedef TileOperand<T, OP == kDweight || OP == kDsumsT ? kAcross : kAlong, BM> A;
     typedef TileOperand<T, LOGITS ? kAlong : kAcross, BN> B;
     constexpr uint32_t LOADS = (A::LOADS + B::LOADS) / WAVES, STAGE = A::BYTES + B::BYTES, KT = kTileK<T>;
@@ -168,9 +169,9 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
     uint32_t m0 = tm * BM, n0 = tn * BN;
     int p = 0;
     if constexpr (!DHIDDEN) {
-        const uint32_t t = OP == kDweight ? tm : tn;
+        const uint32_t t = DWEIGHT ? tm : tn;
         while (p + 1 < a.pieces && t >= a.piece[p + 1].tile) p++;
-        if constexpr (OP == kDweight) m0 = (tm - a.piece[p].tile) * BM;
+        if constexpr (DWEIGHT) m0 = (tm - a.piece[p].tile) * BM;
         else n0 = (tn - a.piece[p].tile) * BN;
     }
     uint32_t t0 = 0, total = a.ktiles;
@@ -188,7 +189,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
         const uint32_t at = wave * LOADS + i;
         if (at < A::LOADS) {
             // across: a piece's columns of G are there up to a multiple of 256
-            const uint32_t last = OP == kDweight || OP == kDsumsT ? 0xffffffffu : a.rows_a - 1 - m0;
+            const uint32_t last = OP == kDweight || OP == kDsumsT ? 0xffffffffu : (OP == kDweightT ? a.piece[p].len : a.rows_a) - 1 - m0;
             A::source(at * 64 + lane, (uint32_t)a.pitch_a, last, off[i], kk[i]);
             kk[i] = 0;
         } else {
@@ -211,6 +212,9 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
         } else if constexpr (OP == kDweight) {
             pa = a.a + (uint64_t)(a.piece[p].col + m0) * T::ESZ + (uint64_t)kt * KT * a.pitch_a;
             pb = a.b + (uint64_t)n0 * T::ESZ + (uint64_t)kt * KT * a.pitch_b;
+        } else if constexpr (OP == kDweightT) {  // the tokens once for each of their two values
+            pa = a.a + (uint64_t)(a.piece[p].col + m0) * a.pitch_a + (uint64_t)kt * kTileRow;
+            pb = a.b + (uint64_t)n0 * T::ESZ + (uint64_t)(kt * KT < a.rows_a ? kt * KT : kt * KT - a.rows_a) * a.pitch_b;
         } else {
             pa = a.a + m0 * a.pitch_a + (uint64_t)kt * kTileRow;
             pb = a.piece[p].w + n0 * a.pitch_b + (uint64_t)kt * kTileRow;
@@ -432,8 +436,8 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
                 });
         } else {
             const float u = a.unscale ? *a.unscale : 1.0f;
-            const uint32_t rows = OP == kDweight ? a.piece[p].len : a.tokens;
-            char* const out = OP == kDweight ? a.piece[p].out : a.out;
+            const uint32_t rows = DWEIGHT ? a.piece[p].len : a.tokens;
+            char* const out = DWEIGHT ? a.piece[p].out : a.out;
             static_assert(WAVES * PART * T::ESZ <= S * STAGE, "the results' way out fits the ring");
             drain<T, MI, NI>(&ring[0][0] + wave * PART * T::ESZ, lane, [&](int i, int j, int e) { return acc[i][j][e] * u; },
                 [&](uint32_t row, uint32_t col, u32x4 x) {
@@ -445,7 +449,8 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
     }
 }
 
-// DWEIGHT of few tokens: a stream of stores.  A wave keeps the hidden states of its NI x
+// DWEIGHT of up to kStreamTokens: a stream of stores (32 tokens, 65536 x 4096 bf16: 114 us of
+// 107 for the bytes; from 64 on tiles take no longer: 166 us of tiles, 172 of this).  A wave keeps the hidden states of its NI x
 // 32 columns in registers and walks a run of the vocabulary, 32 rows at a time, whose
 // rows of G's transpose (`steps` granules a lane, the next 32 rows' under way while these
 // are multiplied) are its other operand.  Neighbouring waves have neighbouring columns
@@ -662,7 +667,7 @@ __global__ __launch_bounds__(256) void k_entropy_pack(PackArgs a, uint32_t width
 
 // What the gradient's products start from, in one launch.  blockIdx.y 0: the tokens'
 // coefficients (one workgroup); 1: the hidden states packed, rows of tokens without
-// gradient zero, so that what those hold reaches no product; 2 (few tokens): their
+// gradient zero, so that what those hold reaches no product; 2 (for k_entropy_dweight_few): their
 // transpose, [width][padded].
 template <class T>
 __global__ __launch_bounds__(256) void k_entropy_prepare(TokenArgs a, const char* hidden, uint32_t width, uint32_t granules,
@@ -738,7 +743,7 @@ __global__ __launch_bounds__(256) void k_entropy_zero(char* out, uint64_t count)
 using namespace host;
 
 constexpr uint64_t kCus = 256;               // of the card this library is built for; plans do not ask the device
-constexpr uint64_t kFewTokens = 128;
+constexpr uint64_t kFewTokens = 128, kStreamTokens = 32;
 constexpr uint64_t kPieceBytes = 128u << 20; // G of one piece of the vocabulary: half the last-level cache
 constexpr uint64_t kPackBytes = 1u << 30;    // packed weights of one piece: enough tiles for all CUs
 
@@ -749,7 +754,7 @@ inline uint64_t up_to(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 template <class T>
 struct EntropyPlan {
     static constexpr uint64_t KT = kTileK<T>;
-    bool few = false;
+    bool few = false, stream = false; // tokens: up to kFewTokens, kStreamTokens
     uint64_t parts = 1, rows = 0;     // of G's elements (few tokens); rows of DHIDDEN's sums, parts of `padded` each
     uint64_t vocab = 0, columns = 0;  // the whole; the same with each rank's rounded up to 256
     uint64_t padded, wide;            // tokens rounded up to 64; elements of a packed row
@@ -779,6 +784,7 @@ struct EntropyPlan {
         }
         wide = up_to(c.width, KT);
         few = gradient && c.tokens <= kFewTokens;
+        stream = gradient && c.tokens <= kStreamTokens;
         padded = few ? (c.tokens <= 32 ? 32 : c.tokens <= 64 ? 64 : 128) : up_to(c.tokens ? c.tokens : 1, 64);
         parts = few && T::ESZ == 2 ? 2 : 1;
         rows = few ? parts * padded : c.tokens;
@@ -804,7 +810,7 @@ struct EntropyPlan {
         at_scale = take(16);
         at_hidden = take(padded * wide * T::ESZ);
         if (pack_weight) at_weight = take(piece * wide * T::ESZ);
-        if (few && c.want_dweight) at_transpose = take(c.width * padded * T::ESZ);
+        if (stream && c.want_dweight) at_transpose = take(c.width * padded * T::ESZ);
         at_g = take(few ? piece * pitch_gt() : padded * pitch_g());
         if (c.want_dhidden) {
             // Few tiles: the contraction is split until each CU has one (256 x 256) or two,
@@ -884,18 +890,19 @@ vrc_status_t launch_entropy(EntropyArgs& a, uint64_t rows, uint64_t cols, bool c
         }
         a.ktiles = t;
     } else {
-        constexpr uint32_t B = OP == kDweight ? BM : BN;
+        constexpr bool DWEIGHT = OP == kDweight || OP == kDweightT;
+        constexpr uint32_t B = DWEIGHT ? BM : BN;
         uint32_t t = 0;
         for (int i = 0; i < a.pieces; i++) {
             a.piece[i].tile = t;
             t += (a.piece[i].len + B - 1) / B;
         }
-        (OP == kDweight ? a.tiles_m : a.tiles_n) = t;
+        (DWEIGHT ? a.tiles_m : a.tiles_n) = t;
     }
     const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
     if (tiles * (WM * WN * 64) > 0xffffffffull) return VRC_ERR_INVALID_ARG;
     const dim3 grid((unsigned)tiles, (unsigned)splits);
-    if constexpr (OP == kDweight) {
+    if constexpr (OP == kDweight || OP == kDweightT) {
         k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
     } else if constexpr (DHIDDEN) {
         k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
@@ -913,7 +920,7 @@ uint64_t tiles_of(const EntropyArgs& a, uint64_t rows, uint64_t cols, uint64_t b
     uint64_t along = 0;
     for (int i = 0; i < a.pieces; i++) along += (a.piece[i].len + b - 1) / b;
     if constexpr (OP == kStats || OP == kGrad) return (rows + b - 1) / b * along;
-    else if constexpr (OP == kDweight) return (cols + b - 1) / b * along;
+    else if constexpr (OP == kDweight || OP == kDweightT) return (cols + b - 1) / b * along;
     else return ((rows + b - 1) / b) * ((cols + b - 1) / b);
 }
 
@@ -956,9 +963,10 @@ vrc_status_t launch_few(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut, 
     return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
 }
 
-template <class T, int STEPS, int NI>
-vrc_status_t launch_dweight_few(EntropyArgs& a, hipStream_t st)
+template <class T>
+vrc_status_t dweight_few(EntropyArgs& a, hipStream_t st)
 {
+    constexpr int STEPS = T::ESZ, NI = T::ESZ == 2 ? 4 : 2;  // steps of 32 bytes
     uint32_t t = 0;
     for (int i = 0; i < a.pieces; i++) {
         a.piece[i].tile = t;
@@ -973,15 +981,6 @@ vrc_status_t launch_dweight_few(EntropyArgs& a, hipStream_t st)
     const uint64_t waves = runs * a.tiles_n;
     k_entropy_dweight_few<T, STEPS, NI><<<(unsigned)((waves + 7) / 8), 512, 0, st>>>(a, (uint32_t)waves);
     return check_launch();
-}
-
-template <class T>
-vrc_status_t dweight_few(EntropyArgs& a, uint64_t padded, hipStream_t st)
-{
-    constexpr int S = T::ESZ;  // steps of 32 bytes: 16 tokens of 16 bits, 8 of 32
-    if (padded == 32) return launch_dweight_few<T, S, T::ESZ == 2 ? 4 : 2>(a, st);
-    if (padded == 64) return launch_dweight_few<T, 2 * S, T::ESZ == 2 ? 4 : 2>(a, st);
-    return launch_dweight_few<T, 4 * S, 2>(a, st);
 }
 
 // Lanes for a row of granules.
@@ -1094,7 +1093,7 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
     char* const sums = c.workspace + plan.at_sums;
     const TokenArgs tokens = {c.target, c.lse, c.dloss, c.dlse, c.ignore_index, (uint32_t)plan.vocab, (uint32_t)c.tokens, (uint32_t)plan.padded};
     const uint32_t granules = (uint32_t)(plan.wide * T::ESZ / 16), lanes = row_lanes(granules), groups = (uint32_t)plan.padded / (256 / lanes) + 1;
-    k_entropy_prepare<T><<<dim3(groups < 65536 ? groups : 65536, plan.few && c.want_dweight ? 3 : 2), 256, 0, st>>>(
+    k_entropy_prepare<T><<<dim3(groups < 65536 ? groups : 65536, plan.stream && c.want_dweight ? 3 : 2), 256, 0, st>>>(
         tokens, c.hidden, (uint32_t)c.width, granules, lanes, hidden, c.workspace + plan.at_transpose, coef, scale);
     vrc_status_t rc = check_launch();
     if (rc) return rc;
@@ -1145,14 +1144,17 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
         }
         if (c.want_dweight) {
             a.pitch_out = c.width * T::ESZ;
-            if (plan.few) {
+            a.b = hidden;
+            a.pitch_b = plan.wide * T::ESZ;
+            a.granules = (uint32_t)(plan.wide * T::ESZ / 16);
+            if (plan.stream) {
                 a.b = c.workspace + plan.at_transpose;
                 a.pitch_b = plan.padded * T::ESZ;
-                rc = dweight_few<T>(a, plan.padded, st);
+                rc = dweight_few<T>(a, st);
+            } else if (plan.few) {
+                a.ktiles = (uint32_t)(plan.pitch_gt() / kTileRow);
+                rc = launch_tiles<T, kDweightT>(a, 0, c.width, false, st);
             } else {
-                a.b = hidden;
-                a.pitch_b = plan.wide * T::ESZ;
-                a.granules = (uint32_t)(plan.wide * T::ESZ / 16);
                 a.ktiles = (uint32_t)(plan.padded / plan.KT);
                 rc = launch_tiles<T, kDweight>(a, 0, c.width, false, st);
             }
