@@ -23,6 +23,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "vrc_model_host.hpp"
 #include "vrc_tiles.hpp"
 
@@ -30,6 +32,8 @@ namespace vrc {
 namespace {
 
 using host::EntropyCall;
+
+constexpr uint64_t kFewTokens = 128, kStreamTokens = 32;
 
 // kDsums: DHIDDEN's sums, in fp32.  kGradT, kDweightT and kDsumsT: of few tokens, by G's transpose.
 enum EntropyOp { kStats, kGrad, kGradT, kDweight, kDweightT, kDhidden, kDsums, kDsumsT };
@@ -679,15 +683,20 @@ __global__ __launch_bounds__(256) void k_entropy_prepare(TokenArgs a, const char
     } else if (blockIdx.y == 1) {
         const uint32_t per = 256 / lanes, lane = threadIdx.x & (lanes - 1);
         for (uint32_t row = blockIdx.x * per + threadIdx.x / lanes; row < a.padded; row += gridDim.x * per) {
+            // loaded whether the token is live or not: the two do not wait for each other
             const bool has = live(a, row);
             const char* from = hidden + (uint64_t)row * width * T::ESZ;
             for (uint32_t g = lane; g < granules; g += lanes) {
                 u32x4 x = {0, 0, 0, 0};
-                if (has) x = row_granule<T>(from, g, width);
+                if (row < a.tokens) x = row_granule<T>(from, g, width);
+#pragma unroll
+                for (int e = 0; e < 4; e++) x[e] = has ? x[e] : 0;
                 st16<false>(packed + ((uint64_t)row * granules + g) * 16, x);
             }
         }
     } else {
+        static_assert(kStreamTokens <= 64, "a bit of the wave's mask for each token");
+        const uint64_t mask = __ballot(live(a, threadIdx.x & 63));
         const uint32_t each = a.padded / T::VEC;  // granules of a column
         const uint64_t count = (uint64_t)width * each;
         for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < count; i += gridDim.x * 256ull) {
@@ -696,7 +705,9 @@ __global__ __launch_bounds__(256) void k_entropy_prepare(TokenArgs a, const char
 #pragma unroll
             for (uint32_t e = 0; e < T::VEC; e++) {
                 const uint32_t t = g * T::VEC + e;
-                const uint32_t s = live(a, t) ? load_s<T>(hidden + ((uint64_t)t * width + col) * T::ESZ) : 0;
+                uint32_t v = 0;
+                if (a.tokens) v = load_s<T>(hidden + ((uint64_t)(t < a.tokens ? t : a.tokens - 1) * width + col) * T::ESZ);
+                const uint32_t s = mask >> t & 1 ? v : 0;
                 if constexpr (T::ESZ == 4) w[e] = s;
                 else w[e / 2] |= s << (16 * (e & 1));
             }
@@ -706,29 +717,45 @@ __global__ __launch_bounds__(256) void k_entropy_prepare(TokenArgs a, const char
 }
 
 // out = unscale x the sums of every split and, in it, of every part (few tokens: of G
-// rounded and of what that left), in their order, rounded.
-template <class T>
-__global__ __launch_bounds__(256) void k_entropy_join(const float* sums, uint32_t splits, uint32_t parts, uint32_t rows,
-                                                      uint32_t tokens, uint32_t width, uint32_t pitch, const float* unscale,
-                                                      char* out)
+// rounded and of what that left), rounded: in their order within each of RUNS interleaved
+// runs and then of the runs.  16 runs where there are many sums of few values, which one
+// lane would fetch one after the other (3 tokens of 17 values, 109 splits: 27 us).
+template <class T, int RUNS>
+__global__ __launch_bounds__(256) void k_entropy_join(const float* sums, uint32_t count, uint32_t rows, uint32_t tokens,
+                                                      uint32_t width, uint32_t pitch, const float* unscale, char* out)
 {
+    constexpr uint32_t QUADS = 256 / RUNS;
+    __shared__ float part[RUNS > 1 ? RUNS : 1][QUADS][RUNS > 1 ? 4 : 1];
     const float u = *unscale;
-    const uint32_t quads = (width + 3) / 4;
-    for (uint32_t row = blockIdx.y; row < tokens; row += gridDim.y)
-        for (uint32_t q = blockIdx.x * 256 + threadIdx.x; q < quads; q += gridDim.x * 256) {
-            float s[4] = {};
+    const uint32_t c = threadIdx.x % QUADS, run = threadIdx.x / QUADS, q = blockIdx.x * QUADS + c, quads = (width + 3) / 4;
+    for (uint32_t row = blockIdx.y; row < tokens; row += gridDim.y) {
+        float s[4] = {};
+        if (q < quads) {
 #pragma unroll 4
-            for (uint32_t i = 0; i < splits * parts; i++) {
+            for (uint32_t i = run; i < count; i += RUNS) {
                 float v[4];
                 F32::unpack(ld16<false>((const char*)(sums + ((uint64_t)i * rows + row) * pitch + q * 4)), v);
 #pragma unroll
                 for (int e = 0; e < 4; e++) s[e] += v[e];
             }
-            char* const to = out + ((uint64_t)row * width + q * 4) * T::ESZ;
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                if (q * 4 + e < width) store_s<T>(to + e * T::ESZ, T::narrow(s[e] * u));
         }
+        if constexpr (RUNS > 1) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) part[run][c][e] = s[e];
+            __syncthreads();
+            if (run == 0)
+                for (int i = 1; i < RUNS; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) s[e] += part[i][c][e];
+            __syncthreads();
+        }
+        if (run || q >= quads) continue;
+        char* const to = out + ((uint64_t)row * width + q * 4) * T::ESZ;
+        const uint32_t left = width - q * 4;
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (e < (int)left) store_s<T>(to + e * T::ESZ, T::narrow(s[e] * u));
+    }
 }
 
 template <class T>
@@ -743,7 +770,6 @@ __global__ __launch_bounds__(256) void k_entropy_zero(char* out, uint64_t count)
 using namespace host;
 
 constexpr uint64_t kCus = 256;               // of the card this library is built for; plans do not ask the device
-constexpr uint64_t kFewTokens = 128, kStreamTokens = 32;
 constexpr uint64_t kPieceBytes = 128u << 20; // G of one piece of the vocabulary: half the last-level cache
 constexpr uint64_t kPackBytes = 1u << 30;    // packed weights of one piece: enough tiles for all CUs
 
@@ -974,10 +1000,9 @@ vrc_status_t dweight_few(EntropyArgs& a, hipStream_t st)
     }
     a.ktiles = t;
     a.tiles_n = (a.width + NI * 32 - 1) / (NI * 32);
-    // two workgroups of eight waves a CU, but runs of four times 32 rows at least
+    // two workgroups of eight waves a CU
     uint64_t runs = (2 * 8 * kCus + a.tiles_n - 1) / a.tiles_n;
-    const uint64_t most = (t + 3) / 4;
-    runs = runs < most ? runs : most;
+    runs = runs < t ? runs : t;
     const uint64_t waves = runs * a.tiles_n;
     k_entropy_dweight_few<T, STEPS, NI><<<(unsigned)((waves + 7) / 8), 512, 0, st>>>(a, (uint32_t)waves);
     return check_launch();
@@ -1163,9 +1188,16 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
         first = false;
     }
     if (!plan.sums) return VRC_OK;
-    const unsigned gx = (unsigned)((c.width + 1023) / 1024);
-    k_entropy_join<T><<<dim3(gx, (unsigned)(c.tokens < 32768 ? c.tokens : 32768)), 256, 0, st>>>(
-        (const float*)sums, (uint32_t)plan.splits, (uint32_t)plan.parts, (uint32_t)plan.padded_rows(), (uint32_t)c.tokens, (uint32_t)c.width, (uint32_t)plan.wide, scale, c.dhidden);
+    const uint32_t count = (uint32_t)(plan.splits * plan.parts), gy = (uint32_t)(c.tokens < 32768 ? c.tokens : 32768);
+    const auto join = [&](auto runs) {
+        constexpr int RUNS = decltype(runs)::value;
+        constexpr uint64_t COLUMNS = 256 / RUNS * 4;
+        k_entropy_join<T, RUNS><<<dim3((unsigned)((c.width + COLUMNS - 1) / COLUMNS), gy), 256, 0, st>>>(
+            (const float*)sums, count, (uint32_t)plan.padded_rows(), (uint32_t)c.tokens, (uint32_t)c.width, (uint32_t)plan.wide,
+            scale, c.dhidden);
+    };
+    if (count >= 8) join(std::integral_constant<int, 16>{});
+    else join(std::integral_constant<int, 1>{});
     return check_launch();
 }
 

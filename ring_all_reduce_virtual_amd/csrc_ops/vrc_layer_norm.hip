@@ -607,7 +607,9 @@ vrc_status_t norm_typed(const NormCall& c, hipStream_t st)
 uint64_t grad_groups(const NormCall& c)
 {
     const uint64_t rows = most_rows(c), most = kNormPartials / (uint64_t)c.parts;
-    return rows < most ? rows : most;
+    if (rows <= most) return rows;
+    const uint64_t each = (rows + most - 1) / most;  // the same number for all of them
+    return (rows + each - 1) / each;
 }
 
 template <class T, int LANES, int V>
