@@ -607,9 +607,8 @@ vrc_status_t norm_typed(const NormCall& c, hipStream_t st)
 uint64_t grad_groups(const NormCall& c)
 {
     const uint64_t rows = most_rows(c), most = kNormPartials / (uint64_t)c.parts;
-    if (rows <= most) return rows;
-    const uint64_t each = (rows + most - 1) / most;  // the same number for all of them
-    return (rows + each - 1) / each;
+    // up to twice as many rows: two for every one, and fewer partial sums
+    return rows <= most ? rows : rows <= 2 * most ? (rows + 1) / 2 : most;
 }
 
 template <class T, int LANES, int V>
@@ -630,6 +629,7 @@ vrc_status_t norm_grad_rows(const NormCall& c, const NormArgs& a, unsigned group
     const uint64_t v = row_vectors<T>(c.width);
 #define VRC_NORM(LANES, V) return launch_norm_grad<T, LANES, V>(a, groups, c.parts, streams(c, T::ESZ), st)
     if (v <= 64) VRC_NORM(64, 1);
+    if (v <= 128) VRC_NORM(64, 2);
     if (v <= 256) VRC_NORM(256, 1);
     if (v <= 512) VRC_NORM(256, 2);
     if (v <= 1024) VRC_NORM(512, 2);
