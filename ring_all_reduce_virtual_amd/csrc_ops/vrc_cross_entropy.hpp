@@ -578,9 +578,10 @@ __device__ __forceinline__ Coef coef_of(const TokenArgs& a, uint32_t t)
 {
     const long long at = a.target[t];
     const bool none = at == a.ignore, bad = !none && (unsigned long long)at >= a.vocab;
+    const float dloss = a.dloss[t], dlse = a.dlse ? a.dlse[t] : 0.0f;
     Coef c;
-    c.b = none ? 0.0f : a.dloss[t];
-    c.a = c.b + (a.dlse ? a.dlse[t] : 0.0f);
+    c.b = none ? 0.0f : dloss;
+    c.a = c.b + dlse;
     if (bad) c.a = __builtin_nanf("");
     c.lse = a.lse[t];
     c.target = none || bad ? kNoTarget : (uint32_t)at;
@@ -669,29 +670,36 @@ __global__ __launch_bounds__(256) void k_entropy_pack(PackArgs a, uint32_t width
     }
 }
 
-// What the gradient's products start from, in one launch.  blockIdx.y 0: the tokens'
+// What the gradient's products start from, in one launch of 1024 lanes a workgroup (the
+// coefficients' one takes the longest: 4096 tokens 22 us with 256).  blockIdx.y 0: the tokens'
 // coefficients (one workgroup); 1: the hidden states packed, rows of tokens without
 // gradient zero, so that what those hold reaches no product; 2 (for k_entropy_dweight_few): their
 // transpose, [width][padded].
 template <class T>
-__global__ __launch_bounds__(256) void k_entropy_prepare(TokenArgs a, const char* hidden, uint32_t width, uint32_t granules,
+__global__ __launch_bounds__(1024) void k_entropy_prepare(TokenArgs a, const char* hidden, uint32_t width, uint32_t granules,
                                                          uint32_t lanes, char* packed, char* transpose, Coef* coef, float* scale)
 {
-    __shared__ float lds[4];
+    __shared__ float lds[16];
     if (blockIdx.y == 0) {
         if (blockIdx.x == 0) write_coefs<T>(a, coef, scale, lds);
     } else if (blockIdx.y == 1) {
-        const uint32_t per = 256 / lanes, lane = threadIdx.x & (lanes - 1);
+        const uint32_t per = 1024 / lanes, lane = threadIdx.x & (lanes - 1);
         for (uint32_t row = blockIdx.x * per + threadIdx.x / lanes; row < a.padded; row += gridDim.x * per) {
             // loaded whether the token is live or not: the two do not wait for each other
-            const bool has = live(a, row);
             const char* from = hidden + (uint64_t)row * width * T::ESZ;
-            for (uint32_t g = lane; g < granules; g += lanes) {
-                u32x4 x = {0, 0, 0, 0};
-                if (row < a.tokens) x = row_granule<T>(from, g, width);
+            bool has = false;
+            for (uint32_t g = lane; g < granules; g += 4 * lanes) {
+                u32x4 x[4] = {};
 #pragma unroll
-                for (int e = 0; e < 4; e++) x[e] = has ? x[e] : 0;
-                st16<false>(packed + ((uint64_t)row * granules + g) * 16, x);
+                for (uint32_t i = 0; i < 4; i++)
+                    if (row < a.tokens && g + i * lanes < granules) x[i] = row_granule<T>(from, g + i * lanes, width);
+                if (g == lane) has = live(a, row);
+#pragma unroll
+                for (uint32_t i = 0; i < 4; i++) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) x[i][e] = has ? x[i][e] : 0;
+                    if (g + i * lanes < granules) st16<false>(packed + ((uint64_t)row * granules + g + i * lanes) * 16, x[i]);
+                }
             }
         }
     } else {
@@ -699,7 +707,7 @@ __global__ __launch_bounds__(256) void k_entropy_prepare(TokenArgs a, const char
         const uint64_t mask = __ballot(live(a, threadIdx.x & 63));
         const uint32_t each = a.padded / T::VEC;  // granules of a column
         const uint64_t count = (uint64_t)width * each;
-        for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < count; i += gridDim.x * 256ull) {
+        for (uint64_t i = blockIdx.x * 1024ull + threadIdx.x; i < count; i += gridDim.x * 1024ull) {
             const uint32_t g = (uint32_t)(i / width), col = (uint32_t)(i - (uint64_t)g * width);
             uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -1117,8 +1125,8 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
     char* const g = c.workspace + plan.at_g;
     char* const sums = c.workspace + plan.at_sums;
     const TokenArgs tokens = {c.target, c.lse, c.dloss, c.dlse, c.ignore_index, (uint32_t)plan.vocab, (uint32_t)c.tokens, (uint32_t)plan.padded};
-    const uint32_t granules = (uint32_t)(plan.wide * T::ESZ / 16), lanes = row_lanes(granules), groups = (uint32_t)plan.padded / (256 / lanes) + 1;
-    k_entropy_prepare<T><<<dim3(groups < 65536 ? groups : 65536, plan.stream && c.want_dweight ? 3 : 2), 256, 0, st>>>(
+    const uint32_t granules = (uint32_t)(plan.wide * T::ESZ / 16), lanes = row_lanes(granules), groups = (uint32_t)plan.padded / (1024 / lanes) + 1;
+    k_entropy_prepare<T><<<dim3(groups < 65536 ? groups : 65536, plan.stream && c.want_dweight ? 3 : 2), 1024, 0, st>>>(
         tokens, c.hidden, (uint32_t)c.width, granules, lanes, hidden, c.workspace + plan.at_transpose, coef, scale);
     vrc_status_t rc = check_launch();
     if (rc) return rc;
