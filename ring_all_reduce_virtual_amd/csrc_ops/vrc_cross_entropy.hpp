@@ -253,15 +253,50 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
     f32x16 acc[MI][NI] = {};
     const uint32_t wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN), r = lane & 31, half = lane >> 5;
     // A step's operands, one ahead of the matrix instructions.  The scheduling barriers
-    // keep the reads of a step in front of the instructions of the step before it: left
-    // alone, the compiler reads each operand right before its use and waits for it.
+    // keep the reads in front of the step before theirs: left alone, the compiler reads each
+    // operand right before its use.  Transposing reads (LATE) hold their wait, and stand
+    // behind that step.
+    constexpr bool TA = A::TRANSPOSED, TB = B::TRANSPOSED, LATE = TA || TB;
+    constexpr int FRAGS = (TA ? MI : 0) + (TB ? NI : 0);
     u32x4 x[2][MI], y[2][NI];
+    uint32_t places[FRAGS ? FRAGS : 1], base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&ring[0][0];
+    if constexpr (TB)
+#pragma unroll
+        for (int j = 0; j < NI; j++) places[j] = base + A::BYTES + B::across_at(wn + j * 32, lane);
+    if constexpr (TA)
+#pragma unroll
+        for (int i = 0; i < MI; i++) places[(TB ? NI : 0) + i] = base + A::across_at(wm + i * 32, lane);
     const auto settle = [] { __builtin_amdgcn_sched_barrier(0); };
-    const auto read = [&](const char* stage, int s) {
+    // Transposing reads of a step: `count` operands from number `first` on, B's before A's.
+    const auto across = [&](auto count, auto step, auto row, int first, uint32_t at) {
+        constexpr int F = decltype(count)::value, s = decltype(step)::value, ROW = decltype(row)::value;
+        uint32_t from[F];
+        u32x4 out[F];
 #pragma unroll
-        for (int j = 0; j < NI; j++) y[s & 1][j] = B::read(stage + A::BYTES, wn + j * 32, s, lane);
+        for (int f = 0; f < F; f++) from[f] = places[first + f] + at * STAGE;
+        read_across<F, s * 16 * ROW, 4 * ROW>(from, out);
 #pragma unroll
-        for (int i = 0; i < MI; i++) x[s & 1][i] = A::read(stage, wm + i * 32, s, lane);
+        for (int f = 0; f < F; f++) {
+            const int g = first + f;
+            if (TB && g < NI) y[s & 1][g] = out[f];
+            else x[s & 1][TB ? g - NI : g] = out[f];
+        }
+    };
+    const auto read = [&](uint32_t at, auto step) {
+        constexpr int s = decltype(step)::value;
+        const char* stage = ring[at];
+        if constexpr (!TB)
+#pragma unroll
+            for (int j = 0; j < NI; j++) y[s & 1][j] = B::read(stage + A::BYTES, wn + j * 32, s, lane);
+        if constexpr (!TA)
+#pragma unroll
+            for (int i = 0; i < MI; i++) x[s & 1][i] = A::read(stage, wm + i * 32, s, lane);
+        if constexpr (TA && TB && (int)A::ROW == (int)B::ROW) {
+            across(std::integral_constant<int, NI + MI>{}, step, std::integral_constant<int, B::ROW>{}, 0, at);
+        } else {
+            if constexpr (TB) across(std::integral_constant<int, NI>{}, step, std::integral_constant<int, B::ROW>{}, 0, at);
+            if constexpr (TA) across(std::integral_constant<int, MI>{}, step, std::integral_constant<int, A::ROW>{}, TB ? NI : 0, at);
+        }
         settle();
     };
     const auto multiply = [&](int s, int i) {
@@ -280,14 +315,18 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
         wait_vmem_below<LOADS*(S - 1)>();
         tile_barrier();
         uint32_t cur = 0;
-        read(ring[0], 0);
+        typedef std::integral_constant<int, 0> First;
+        read(0, First{});
+        const auto one = [&](auto next) {  // the step before `next`, and its operands
+            constexpr int s = decltype(next)::value;
+            if constexpr (LATE) step(s - 1);
+            read(cur, next);
+            if constexpr (!LATE) step(s - 1);
+        };
         const auto first_steps = [&] {
-            read(ring[cur], 1);
-            step(0);
-            read(ring[cur], 2);
-            step(1);
-            read(ring[cur], 3);
-            step(2);
+            one(std::integral_constant<int, 1>{});
+            one(std::integral_constant<int, 2>{});
+            one(std::integral_constant<int, 3>{});
         };
         for (uint32_t t = 1; t < total; t++) {
             aim();
@@ -296,7 +335,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
             wait_vmem_below<LOADS*(S - 2)>();
             tile_barrier();
             cur = cur + 1 == S ? 0 : cur + 1;
-            read(ring[cur], 0);
+            if constexpr (!LATE) read(cur, First{});
             // the loads between the matrix instructions of the last step
 #pragma unroll
             for (int i = 0; i < MI; i++) {
@@ -307,6 +346,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
                 settle();
             }
             advance();
+            if constexpr (LATE) read(cur, First{});
         }
         first_steps();
         step(3);

@@ -75,6 +75,48 @@ __device__ __forceinline__ void xcd_tile(uint32_t b, uint32_t tiles_m, uint32_t 
     tn = i / rows;
 }
 
+// F matrix operands of 16-bit elements read across: for each, two transposing reads of four
+// rows at a lane's address `at` and at OFF and STEP bytes behind it.  As assembly with its own
+// wait: the compiler takes the builtin for an access that direct loads to LDS may write, and
+// waits for all of those, the next tile's, before every one (4096 x 16384 x 4096: the
+// weights' gradients 528 us with the builtin, 460 with this).  The tile's barrier orders both.
+template <int F, int OFF, int STEP>
+__device__ __forceinline__ void read_across(const uint32_t (&at)[F], u32x4 (&out)[F])
+{
+    u32x2 a[F], b[F];
+#define VRC_TR(d, s, o) "ds_read_b64_tr_b16 %" #d ", %" #s " offset:%" #o "\n\t"
+    static_assert(F == 1 || F == 2 || F == 3 || F == 4 || F == 6, "operands of a wave");
+    if constexpr (F == 1) {
+        __asm__ volatile(VRC_TR(0, 2, 3) VRC_TR(1, 2, 4) "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(a[0]), "=&v"(b[0]) : "v"(at[0]), "n"(OFF), "n"(OFF + STEP) : "memory");
+    } else if constexpr (F == 2) {
+        __asm__ volatile(VRC_TR(0, 4, 6) VRC_TR(1, 4, 7) VRC_TR(2, 5, 6) VRC_TR(3, 5, 7) "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(a[0]), "=&v"(b[0]), "=&v"(a[1]), "=&v"(b[1])
+                         : "v"(at[0]), "v"(at[1]), "n"(OFF), "n"(OFF + STEP) : "memory");
+    } else if constexpr (F == 3) {
+        __asm__ volatile(VRC_TR(0, 6, 9) VRC_TR(1, 6, 10) VRC_TR(2, 7, 9) VRC_TR(3, 7, 10) VRC_TR(4, 8, 9) VRC_TR(5, 8, 10)
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(a[0]), "=&v"(b[0]), "=&v"(a[1]), "=&v"(b[1]), "=&v"(a[2]), "=&v"(b[2])
+                         : "v"(at[0]), "v"(at[1]), "v"(at[2]), "n"(OFF), "n"(OFF + STEP) : "memory");
+    } else if constexpr (F == 4) {
+        __asm__ volatile(VRC_TR(0, 8, 12) VRC_TR(1, 8, 13) VRC_TR(2, 9, 12) VRC_TR(3, 9, 13) VRC_TR(4, 10, 12) VRC_TR(5, 10, 13)
+                         VRC_TR(6, 11, 12) VRC_TR(7, 11, 13) "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(a[0]), "=&v"(b[0]), "=&v"(a[1]), "=&v"(b[1]), "=&v"(a[2]), "=&v"(b[2]), "=&v"(a[3]), "=&v"(b[3])
+                         : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF), "n"(OFF + STEP) : "memory");
+    } else {
+        __asm__ volatile(VRC_TR(0, 12, 18) VRC_TR(1, 12, 19) VRC_TR(2, 13, 18) VRC_TR(3, 13, 19) VRC_TR(4, 14, 18) VRC_TR(5, 14, 19)
+                         VRC_TR(6, 15, 18) VRC_TR(7, 15, 19) VRC_TR(8, 16, 18) VRC_TR(9, 16, 19) VRC_TR(10, 17, 18) VRC_TR(11, 17, 19)
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(a[0]), "=&v"(b[0]), "=&v"(a[1]), "=&v"(b[1]), "=&v"(a[2]), "=&v"(b[2]), "=&v"(a[3]), "=&v"(b[3]),
+                           "=&v"(a[4]), "=&v"(b[4]), "=&v"(a[5]), "=&v"(b[5])
+                         : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "n"(OFF), "n"(OFF + STEP)
+                         : "memory");
+    }
+#undef VRC_TR
+#pragma unroll
+    for (int f = 0; f < F; f++) out[f] = u32x4{a[f].x, a[f].y, b[f].x, b[f].y};
+}
+
 // One operand of a tile: B rows (ALONG) or columns (ACROSS).
 template <class T, int KIND, int B>
 struct TileOperand {
@@ -109,7 +151,16 @@ struct TileOperand {
         }
     }
 
-    // A lane's operand of step s (of four): rows or columns c0 .. c0 + 31, one a lane;
+    // ACROSS of 16 bits: what read_across() takes of columns c0 .. c0 + 31 at step 0; a
+    // step is 16 rows on.
+    static constexpr bool TRANSPOSED = KIND == kAcross && T::ESZ == 2;
+    static __device__ __forceinline__ uint32_t across_at(uint32_t c0, uint32_t lane)
+    {
+        const uint32_t j = lane & 15, k = 8 * (lane >> 5) + j / 4;
+        return k * ROW + run_place(c0 / 32, k) * RUN + (lane >> 4 & 1) * 32 + (j & 3) * 8;
+    }
+
+    // Else a lane's operand of step s (of four): rows or columns c0 .. c0 + 31, one a lane;
     // elements 2 s + half granules on.
     static __device__ __forceinline__ u32x4 read(const char* stage, uint32_t c0, int s, uint32_t lane)
     {
@@ -117,14 +168,6 @@ struct TileOperand {
         if constexpr (KIND == kAlong) {
             const uint32_t row = c0 + (lane & 31);
             return *(const u32x4*)(stage + row * kTileRow + (((2 * s + half) ^ (row >> 1 & 7)) * 16));
-        } else if constexpr (T::ESZ == 2) {
-            const uint32_t j = lane & 15, k = 16 * s + 8 * half + j / 4;
-            const char* at = stage + k * ROW + run_place(c0 / 32, k) * RUN + (lane >> 4 & 1) * 32 + (j & 3) * 8;
-            typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
-            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 4 * ROW));
-            const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
-            return u32x4{x.x, x.y, y.x, y.y};
         } else {
             const uint32_t k = 8 * s + 4 * half;
             const char* at = stage + k * ROW + run_place(c0 / 32, k) * RUN + (lane & 31) * 4;
