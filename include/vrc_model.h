@@ -61,7 +61,8 @@ typedef struct {
  *   mean, rstd  NULL, or `parts` arrays of fp32, one value per row.  mean is NULL
  *             where not centred.
  * recv[r] may be send[r] itself (not for VRC_NORM_SCATTER), sum[p] may be
- * residual[p] itself; outputs overlap nothing else.
+ * residual[p] itself; outputs overlap nothing else.  width < 2^26; rows of up to 16384
+ * values are read once, longer ones once for each pass over them.
  */
 vrc_status_t vrc_layer_norm(const vrc_layer_norm_t* norm, const void* const* send, const void* const* residual,
                             const void* weight, const void* bias, void* const* recv, void* const* sum,
@@ -112,8 +113,9 @@ typedef struct {
 /*
  *   hidden  [tokens, width], which all ranks share; target [tokens], 64-bit.
  *   loss, lse  [tokens] of fp32; loss may be NULL (and target then too).
- * An empty vocabulary gives lse -infinity.  tokens, width and the sum of vocab are
- * below 2^31.
+ * An empty vocabulary gives lse -infinity.
+ * tokens < 2^24, width from 1 to 2^20 - 1, the sum of vocab < 2^23, and tokens and the sum
+ * of vocab times width < 2^37 (VRC_ERR_INVALID_ARG otherwise).
  */
 vrc_status_t vrc_cross_entropy(const vrc_cross_entropy_t* ce, const void* hidden, const void* const* weight,
                                const long long* target, float* loss, float* lse, int nranks, void* workspace,

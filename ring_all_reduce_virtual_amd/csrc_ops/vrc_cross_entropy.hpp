@@ -974,7 +974,7 @@ vrc_status_t launch_entropy(EntropyArgs& a, uint64_t rows, uint64_t cols, bool c
         (DWEIGHT ? a.tiles_m : a.tiles_n) = t;
     }
     const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
-    if (tiles * (WM * WN * 64) > 0xffffffffull) return VRC_ERR_INVALID_ARG;
+    if (tiles * (WM * WN * 64) > 0xffffffffull) return VRC_ERR_INVALID_ARG;  // not with sizes that the entry points let pass
     const dim3 grid((unsigned)tiles, (unsigned)splits);
     if constexpr (OP == kDweight || OP == kDweightT) {
         k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);

@@ -40,7 +40,7 @@ vrc_status_t norm_call(const vrc_layer_norm_t* d, int n, NormCall* c, vrc_dtype_
     if (!float_dtype(dtype) || (wdtype != dtype && wdtype != VRC_FP32)) return VRC_ERR_UNSUPPORTED;
     if (join != VRC_NORM_EACH && join != VRC_NORM_SUM && join != VRC_NORM_SCATTER) return VRC_ERR_UNSUPPORTED;
     if (!(d->eps >= 0.0) || std::isinf(d->eps)) return VRC_ERR_INVALID_ARG;
-    if (d->width >= 1ull << 31 || d->rows > kMaxCount || (d->width && d->rows > kMaxCount / d->width)) return VRC_ERR_INVALID_ARG;
+    if (d->width >= 1ull << 26 || d->rows > kMaxCount || (d->width && d->rows > kMaxCount / d->width)) return VRC_ERR_INVALID_ARG;
     c->rows = d->rows;
     c->width = d->width;
     c->eps = d->eps;
@@ -181,16 +181,18 @@ vrc_status_t entropy_call(const vrc_cross_entropy_t* d, const void* hidden, cons
     if (!d || n < 1 || n > kMaxRanks || !d->vocab) return VRC_ERR_INVALID_ARG;
     const int dtype = raw(d->dtype);
     if (!float_dtype(dtype)) return VRC_ERR_UNSUPPORTED;
-    if (d->tokens >= 1ull << 31 || d->width == 0 || d->width >= 1ull << 20) return VRC_ERR_INVALID_ARG;
+    // what grids and 32-bit offsets within a tile hold
+    if (d->tokens >= 1ull << 24 || d->width == 0 || d->width >= 1ull << 20) return VRC_ERR_INVALID_ARG;
     uint64_t total = 0;
     for (int r = 0; r < n; r++) {
-        if (d->vocab[r] >= 1ull << 31) return VRC_ERR_INVALID_ARG;
+        if (d->vocab[r] >= 1ull << 23) return VRC_ERR_INVALID_ARG;
         c->vocab[r] = d->vocab[r];
         total += d->vocab[r];
         if (d->vocab[r] && (!weight || !weight[r])) return VRC_ERR_INVALID_ARG;
         c->weight[r] = weight ? (const char*)weight[r] : nullptr;
     }
-    if (total >= 1ull << 31 || (d->tokens && !hidden)) return VRC_ERR_INVALID_ARG;
+    if (total >= 1ull << 23 || (d->tokens && !hidden)) return VRC_ERR_INVALID_ARG;
+    if (total * d->width >= 1ull << 37 || d->tokens * d->width >= 1ull << 37) return VRC_ERR_INVALID_ARG;
     c->hidden = (const char*)hidden;
     c->tokens = d->tokens;
     c->width = d->width;

@@ -53,7 +53,7 @@ def test_layer_norm_refusals():
     assert f(n=0) == f(n=17) == f(d=None) == f(x=None) == f(y=None) == f(w=None) == INVALID
     assert f(x=vrc._ptr_array([A, None, A, A])) == f(y=vrc._ptr_array([B, None, R, R])) == INVALID
     assert f(d=norm(eps=-1.0)) == f(d=norm(eps=float("nan"))) == f(d=norm(eps=float("inf"))) == INVALID
-    assert f(d=norm(width=1 << 31)) == f(d=norm(rows=1 << 57)) == f(d=norm(rows=1 << 40, width=1 << 20)) == INVALID
+    assert f(d=norm(width=1 << 26)) == f(d=norm(rows=1 << 57)) == f(d=norm(rows=1 << 40, width=1 << 20)) == INVALID
     assert f(d=norm(dt=vrc.VRC_INT32)) == f(d=norm(dt=9)) == f(d=norm(wdt=vrc.VRC_FP16)) == UNSUPPORTED
     assert f(d=norm(join=3)) == f(d=norm(join=-1)) == UNSUPPORTED
     assert f(d=norm(center=0), mean=arr(R)) == INVALID                       # RMS norm has no mean
@@ -112,8 +112,9 @@ def test_cross_entropy_refusals():
 
     assert f(n=0) == f(n=17) == f(h=None) == f(w=None) == f(t=None) == f(lse=None) == f(w=vrc._ptr_array([B, None])) == INVALID
     assert L.vrc_cross_entropy(None, A, arr(B, 2), R, S, T, 2, W, 1 << 28, None) == INVALID
-    assert f(d=ce(width=0)) == f(d=ce(width=1 << 20)) == f(d=ce(tokens=1 << 31)) == INVALID
-    assert f(d=ce(vocab=(1 << 31, 1))) == f(d=ce(vocab=(1 << 30, 1 << 30))) == INVALID
+    assert f(d=ce(width=0)) == f(d=ce(width=1 << 20)) == f(d=ce(tokens=1 << 24)) == INVALID
+    assert f(d=ce(vocab=(1 << 23, 1))) == f(d=ce(vocab=(1 << 22, 1 << 22))) == INVALID
+    assert f(d=ce(width=1 << 19, vocab=(1 << 18, 0))) == f(d=ce(width=1 << 19, tokens=1 << 18)) == INVALID
     assert f(d=ce(dt=vrc.VRC_INT32)) == f(d=ce(dt=7)) == UNSUPPORTED
     assert f(t=R + 4) == f(lse=T + 2) == f(ws=W + 8) == f(ws=None) == f(size=entropy_space(ce(), 2, False) - 1) == INVALID
     assert f(lse=A) == f(loss=B + 64) == f(loss=T) == f(ws=R) == f(ws=S) == f(lse=R) == ALIAS
