@@ -153,10 +153,13 @@ __device__ __forceinline__ float exp_of(float x)
 // loads under way, which is what its waits count.
 // CUT (LOGITS): B's elements past the end of a row are read from a constant zero (A's
 // are zero in memory).
-template <class T, int OP, int BM, int BN, int WM, int WN, int S, bool CUT>
-__global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
+// KS: 1, or 4 groups of waves that each take one step of every tile of the contraction, and
+// join their sums in LDS (ALONG operands): where the matrix instructions bound and tiles are
+// few, smaller ones then fill the CUs.
+template <class T, int OP, int BM, int BN, int WM, int WN, int S, bool CUT, int KS>
+__global__ __launch_bounds__(WM * WN * KS * 64) void k_entropy(EntropyArgs a)
 {
-    constexpr int MI = BM / WM / 32, NI = BN / WN / 32, WAVES = WM * WN;
+    constexpr int MI = BM / WM / 32, NI = BN / WN / 32, WAVES = WM * WN * KS;
     constexpr bool DHIDDEN = OP == kDhidden || OP == kDsums || OP == kDsumsT, LOGITS = OP == kStats || OP == kGrad || OP == kGradT;
     constexpr bool DWEIGHT = OP == kDweight || OP == kDweightT;
     typedef TileOperand<T, OP == kDweight || OP == kDsumsT ? kAcross : kAlong, BM> A;
@@ -251,7 +254,8 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
     };
 
     f32x16 acc[MI][NI] = {};
-    const uint32_t wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN), r = lane & 31, half = lane >> 5;
+    const uint32_t member = wave % (WM * WN), group = wave / (WM * WN);
+    const uint32_t wm = member % WM * (BM / WM), wn = member / WM * (BN / WN), r = lane & 31, half = lane >> 5;
     // A step's operands, one ahead of the matrix instructions.  The scheduling barriers
     // keep the reads in front of the step before theirs: left alone, the compiler reads each
     // operand right before its use.  Transposing reads (LATE) hold their wait, and stand
@@ -309,7 +313,62 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
         for (int i = 0; i < MI; i++) multiply(s, i);
         settle();
     };
-    if (total) {
+    if constexpr (KS == 4) {
+        static_assert(!LATE, "a step by number");
+        const auto mine = [&](uint32_t at) {
+#pragma unroll
+            for (int j = 0; j < NI; j++) y[0][j] = B::read(ring[at] + A::BYTES, wn + j * 32, group, lane);
+#pragma unroll
+            for (int i = 0; i < MI; i++) x[0][i] = A::read(ring[at], wm + i * 32, group, lane);
+            settle();
+        };
+        if (total) {
+#pragma unroll
+            for (int t = 0; t < S; t++) fetch();
+            wait_vmem_below<LOADS*(S - 1)>();
+            tile_barrier();
+            uint32_t cur = 0;
+            mine(0);
+            for (uint32_t t = 1; t < total; t++) {
+                aim();
+                wait_vmem_below<LOADS*(S - 2)>();
+                tile_barrier();
+                cur = cur + 1 == S ? 0 : cur + 1;
+#pragma unroll
+                for (uint32_t i = 0; i < LOADS; i++) load(i);
+                advance();
+                step(0);
+                mine(cur);
+            }
+            step(0);
+            wait_vmem_below<0>();
+        }
+        __syncthreads();
+        static_assert((KS - 1) * WM * WN * MI * NI * 4096 <= S * STAGE, "the groups' sums fit the ring");
+        char* const sums = &ring[0][0] + member * (MI * NI * 4096) + lane * 16;
+        if (group) {
+#pragma unroll
+            for (int i = 0; i < MI * NI; i++)
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    const f32x16& v = acc[i / NI][i % NI];
+                    *(u32x4*)(sums + ((group - 1) * WM * WN * MI * NI + i) * 4096 + g * 1024) =
+                        u32x4{__float_as_uint(v[4 * g]), __float_as_uint(v[4 * g + 1]), __float_as_uint(v[4 * g + 2]), __float_as_uint(v[4 * g + 3])};
+                }
+        }
+        __syncthreads();
+        if (group == 0)
+            for (int k = 0; k < KS - 1; k++)
+#pragma unroll
+                for (int i = 0; i < MI * NI; i++)
+#pragma unroll
+                    for (int g = 0; g < 4; g++) {
+                        float v[4];
+                        F32::unpack(*(const u32x4*)(sums + (k * WM * WN * MI * NI + i) * 4096 + g * 1024), v);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) acc[i / NI][i % NI][4 * g + e] += v[e];
+                    }
+    } else if (total) {
 #pragma unroll
         for (int t = 0; t < S; t++) fetch();
         wait_vmem_below<LOADS*(S - 1)>();
@@ -358,7 +417,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
         const uint32_t cols = a.piece[p].len - n0;  // that the tile has
         float2* const part = (float2*)&ring[0][0];  // [WN][BM]
 #pragma unroll
-        for (int i = 0; i < MI; i++) {
+        for (int i = 0; i < (KS > 1 && group ? 0 : MI); i++) {
             float top = -INFINITY, sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < NI; j++)
@@ -375,7 +434,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
 #pragma unroll
                 for (int e = 0; e < 16; e++) sum += exp_of<T>(acc[i][j][e] - from);
             sum += __shfl_xor(sum, 32, 64);
-            if (half == 0) part[wave / WM * BM + wm + i * 32 + r] = make_float2(top, sum);
+            if (half == 0) part[member / WM * BM + wm + i * 32 + r] = make_float2(top, sum);
             const uint32_t token = m0 + wm + i * 32 + r;
             if (a.target && token < a.tokens) {
                 const unsigned long long at = (unsigned long long)a.target[token] - a.piece[p].first - n0 - wn;
@@ -432,6 +491,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_entropy(EntropyArgs a)
         } else if constexpr (OP == kGradT) {
             // a lane has a row of the transpose, four consecutive tokens at a time
             const uint32_t cols = a.piece[p].len - n0;
+            if (KS > 1 && group) return;
 #pragma unroll
             for (int i = 0; i < MI; i++)
 #pragma unroll
@@ -872,7 +932,7 @@ struct EntropyPlan {
             tokens = c.tokens < 16384 ? c.tokens : 16384;
             if (pack_hidden) at_hidden = take(c.tokens * wide * T::ESZ);
             if (pack_weight) at_weight = take(piece * wide * T::ESZ);
-            at_stats = take((columns / 64) * tokens * sizeof(float2));
+            at_stats = take(columns / (T::ESZ == 4 && tokens <= 64 ? 32 : 64) * tokens * sizeof(float2));
             at_picked = take(tokens * sizeof(float));
             return;
         }
@@ -950,7 +1010,7 @@ struct PieceWalk {
     }
 };
 
-template <class T, int OP, int BM, int BN, int WM, int WN, int S>
+template <class T, int OP, int BM, int BN, int WM, int WN, int S, int KS = 1>
 vrc_status_t launch_entropy(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut, int splits, hipStream_t st)
 {
     a.tiles_m = (uint32_t)((rows + BM - 1) / BM);
@@ -974,15 +1034,16 @@ vrc_status_t launch_entropy(EntropyArgs& a, uint64_t rows, uint64_t cols, bool c
         (DWEIGHT ? a.tiles_m : a.tiles_n) = t;
     }
     const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n;
-    if (tiles * (WM * WN * 64) > 0xffffffffull) return VRC_ERR_INVALID_ARG;  // not with sizes that the entry points let pass
+    constexpr int LANES = WM * WN * KS * 64;
+    if (tiles * LANES > 0xffffffffull) return VRC_ERR_INVALID_ARG;  // not with sizes that the entry points let pass
     const dim3 grid((unsigned)tiles, (unsigned)splits);
     if constexpr (OP == kDweight || OP == kDweightT) {
-        k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
+        k_entropy<T, OP, BM, BN, WM, WN, S, false, KS><<<grid, LANES, 0, st>>>(a);
     } else if constexpr (DHIDDEN) {
-        k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
+        k_entropy<T, OP, BM, BN, WM, WN, S, false, KS><<<grid, LANES, 0, st>>>(a);
     } else {
-        if (cut) k_entropy<T, OP, BM, BN, WM, WN, S, true><<<grid, WM * WN * 64, 0, st>>>(a);
-        else k_entropy<T, OP, BM, BN, WM, WN, S, false><<<grid, WM * WN * 64, 0, st>>>(a);
+        if (cut) k_entropy<T, OP, BM, BN, WM, WN, S, true, KS><<<grid, LANES, 0, st>>>(a);
+        else k_entropy<T, OP, BM, BN, WM, WN, S, false, KS><<<grid, LANES, 0, st>>>(a);
     }
     return check_launch();
 }
@@ -1030,6 +1091,15 @@ vrc_status_t launch_tiles(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut
 template <class T, int OP>
 vrc_status_t launch_few(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut, int splits, hipStream_t st)
 {
+    // fp32's are bound by the matrix instructions: where tiles of 128 columns leave CUs idle, of
+    // 32 by four waves that share the contraction (28 x 191 x 768 20 -> 10.5 us, 48 x 20011 x 1000
+    // 46 -> 43; but 64 x 65536 x 4096 305 -> 325)
+    if (T::ESZ == 4 && OP != kDsumsT && tiles_of<kStats>(a, rows, cols, 128) <= kCus) {
+        if constexpr (T::ESZ == 4 && OP != kDsumsT) {
+            if (rows <= 32) return launch_entropy<T, OP, 32, 32, 1, 1, 4, 4>(a, rows, cols, cut, splits, st);
+            if (rows <= 64) return launch_entropy<T, OP, 64, 32, 1, 1, 4, 4>(a, rows, cols, cut, splits, st);
+        }
+    }
     if (rows <= 32) return launch_entropy<T, OP, 32, 128, 1, 4, 4>(a, rows, cols, cut, splits, st);
     if (rows <= 64) return launch_entropy<T, OP, 64, 128, 1, 4, 3>(a, rows, cols, cut, splits, st);
     if constexpr (OP == kDsumsT && T::ESZ == 2)
