@@ -19,6 +19,12 @@
 // two values each, G rounded and what that left: the matrix cores have the time, and the
 // rounding of a few large elements of G does not average out as it does over many tokens
 // (7 tokens: errors of the weights' gradients 0.0028 of their norm, bf16's own rounding 0.0017).
+//
+// Measured on MI355X, 4096 tokens and 8 x (8192 x 4096) bf16, calls one after the other on other
+// inputs: the loss 1,732 us (1.27 PFLOP/s, matrix pipes busy for 70 % of all cycles), the gradients
+// 5,369 us (1.23 PFLOP/s: for each of four pieces LOGITS 448, DHIDDEN 460, DWEIGHT 435 us).
+// One token 106 us for 537 MB; the gradients of 7 tokens, 8 x (4096 x 4096), 171 us (LOGITS 57,
+// DHIDDEN 53, DWEIGHT 51).  fp32, 2048 x 16384 x 2048: 138 TFLOP/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
