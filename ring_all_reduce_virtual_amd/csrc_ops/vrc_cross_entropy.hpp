@@ -1072,7 +1072,8 @@ template <class T, class Tiles>
 int tile_side(Tiles tiles)
 {
     if (tiles(64) <= 2 * kCus) return 64;
-    return T::ESZ == 4 || tiles(128) <= 2 * kCus ? 128 : 256;
+    if (T::ESZ == 4) return tiles(64) * 10 < tiles(128) * 36 ? 64 : 128;
+    return tiles(128) <= 2 * kCus ? 128 : 256;
 }
 
 // The product, by tiles of one side.
@@ -1161,7 +1162,7 @@ vrc_status_t pack_pieces(const EntropyCall& c, const EntropyPlan<T>& plan, Entro
         p.src[i] = a.piece[i].w;
         p.dst[i] = to;
         p.rows[i] = p.padded[i] = a.piece[i].len;
-        a.piece[i].w = to;
+        a.piece[i].w = to;  // one behind the other
         to += (uint64_t)a.piece[i].len * plan.wide * T::ESZ;
     }
     return pack<T>(p, a.pieces, c.width, plan.wide, st);
@@ -1193,6 +1194,9 @@ vrc_status_t cross_entropy_typed(const EntropyCall& c, hipStream_t st)
             if (plan.pack_weight) {
                 const vrc_status_t rc = pack_pieces(c, plan, a, st);
                 if (rc) return rc;
+                // packed they are one matrix, whose tiles cross the ranks' ends
+                for (int i = 1; i < a.pieces; i++) a.piece[0].len += a.piece[i].len;
+                a.pieces = 1;
             }
             a.pitch_a = (plan.pack_hidden ? plan.wide : c.width) * T::ESZ;
             a.pitch_b = (plan.pack_weight ? plan.wide : c.width) * T::ESZ;
