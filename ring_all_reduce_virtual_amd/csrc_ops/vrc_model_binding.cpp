@@ -323,7 +323,10 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count)
         const vrc_layer_norm_t d = norm_of(s, l, w, join, center, number(a[3]));
         const vrc_stream_t st = stream_of(a[9], l);
         Ref ys = outputs(a[7], s.outs, l.type, l, false, where, "recv", y);
-        Ref hs = added ? outputs(a[8], s.parts, l.type, l, s.one, where, "sum", h) : (Py_INCREF(a[0]), Ref(a[0]));
+        // rows that nothing is added to are their own sum, unless y takes their place
+        bool over = false;
+        for (int r = 0; r < n && !added; r++) over |= s.rows && s.width && y[r] == x[r];
+        Ref hs = added ? outputs(a[8], s.parts, l.type, l, s.one, where, "sum", h) : over ? Ref(none()) : (Py_INCREF(a[0]), Ref(a[0]));
         Ref means = center ? allocate(s.lines, at::kFloat, l, s.one, mean) : Ref(none());
         Ref rstds = allocate(s.lines, at::kFloat, l, s.one, rstd);
         call(where, [&] {

@@ -13,6 +13,7 @@ import ctypes as C
 import importlib.machinery
 import importlib.util
 import os
+import threading
 
 from . import PKG, VRC_OK, VrcError, _stream, _torch
 from .ops import OPS_VERSION, _on, _ops
@@ -58,12 +59,19 @@ def _failed(status: int, where: str):
 
 
 _module = None
+_loading = threading.Lock()
 
 
 def _native():
     """The compiled module, loaded by the first call (it needs torch, as the tensors do)."""
+    return _module or _load()
+
+
+def _load():
     global _module
-    if _module is None:
+    with _loading:
+        if _module is not None:
+            return _module
         torch = _torch()
         if not os.path.exists(MODEL_BINDING_PATH):
             raise ImportError(f"{MODEL_BINDING_PATH} is missing: build the HIP libraries first "
@@ -75,7 +83,7 @@ def _native():
         if version != OPS_VERSION:
             raise ImportError(f"{MODEL_BINDING_PATH} reports version {version}, this binding needs {OPS_VERSION}: rebuild it")
         _module = module
-    return _module
+        return module
 
 
 def _run(call, where, first, stream, args):
@@ -111,7 +119,7 @@ def vrc_layer_norm(send, weight, bias=None, eps=1e-5, residual=None, join="each"
 
     ``weight`` and ``bias`` are of the rows' dtype or float32.  h is rounded from the
     fp32 values that y is computed from (without anything added, ``"each"`` returns
-    ``send`` itself); mean and rstd are float32, one per row, mean None where not
+    ``send`` itself, or None where ``recv`` overwrites it); mean and rstd are float32, one per row, mean None where not
     centred.  ``recv=send`` (not for ``"scatter"``) and ``sum=residual``, where h goes,
     run in place.  Gradient: ``vrc_layer_norm_grad``."""
     return _run(_native().layer_norm, "vrc_layer_norm", send, stream,

@@ -123,6 +123,36 @@ def test_empty_calls(vrc):
     assert not dh.any() and all(d.shape == (0, 16) for d in dw)
 
 
+def test_one_row_and_one_token_without_leading_dimensions(vrc):
+    f = gen(2)
+    x, w, b = f(100), f(100), f(100)
+    y, h, mean, rstd = vrc.vrc_layer_norm([x, x], w, b, join="sum")
+    assert y[0].shape == h.shape == (100,) and mean.shape == rstd.shape == ()
+    want = ref.layer_norm([x, x], None, w, b, 1e-5, True)
+    close(y[1], want[0], "y")
+    dx, dw, db = vrc.vrc_layer_norm_grad([x, x], h, w, mean, rstd, join="sum")
+    assert dx[0].shape == dw.shape == db.shape == (100,)
+    t = torch.tensor(3, device=DEV)
+    loss, lse = vrc.vrc_cross_entropy(x, [f(7, 100)], t)
+    assert loss.shape == lse.shape == ()
+    dh, _ = vrc.vrc_cross_entropy_grad(x, [f(7, 100)], t, lse, torch.ones_like(loss))
+    assert dh.shape == (100,)
+    loss3, lse3 = vrc.vrc_cross_entropy(f(2, 3, 100), [f(7, 100)], torch.zeros(2, 3, dtype=torch.int64, device=DEV))
+    assert loss3.shape == lse3.shape == (2, 3)
+
+
+def test_rows_that_y_overwrites_are_not_returned_as_h(vrc):
+    """Without a residual each rank's rows are h; in place they are gone."""
+    x, _, w, b = norm_inputs("each", 2, 4, 64, torch.float32, 14)
+    want = vrc.vrc_layer_norm(x, w, b)
+    assert want[1] is x
+    rows = [t.clone() for t in x]
+    y, h, mean, rstd = vrc.vrc_layer_norm(rows, w, b, recv=rows)
+    assert y is rows and h is None
+    same([want[0], want[2], want[3]], [y, mean, rstd])
+    assert vrc.vrc_layer_norm(x, w, b, recv=[torch.empty_like(t) for t in x])[1] is x
+
+
 # ---------------------------------------------------------------------------
 # Values
 # ---------------------------------------------------------------------------
