@@ -135,10 +135,10 @@ struct RowIo {
                 float f[4];
                 F32::unpack(x, f);
 #pragma unroll
-                for (int e = 0; e < 4; e++) p.v[j * T::VEC + q * 4 + e] = f[e];
+                for (int e = 0; e < 4; e++) p.v[j * T::VEC + q * 4 + e] = has[j] ? f[e] : 0.0f;
             }
         p.t = 0.0f;
-        if (tail) p.t = F32::widen(load_s<F32>(w + tail_at * UP));
+        if (tail) p.t = has_tail ? F32::widen(load_s<F32>(w + tail_at * UP)) : 0.0f;
     }
 };
 
@@ -301,13 +301,15 @@ __global__ __launch_bounds__(block_of(LANES), ONE && LANES == 512 && V == 2 ? 4 
         const float mean = a.center ? a.mean[r][i] : 0.0f, rstd = a.rstd[r][i];
         if constexpr (ONE) io.widen(io.load(a.src[each ? r : 0] + (mine.first + i) * pitch), dy);
         else fold_all<(V <= 2 ? 4 : 2)>(io, [&](int q) { return a.src[each ? r : q] + (mine.first + i) * pitch; }, ranks, dy);
-        // x of vector j: computed twice from h, whose 16-bit values take half the registers
+        // x of vector j: computed twice from h, whose 16-bit values take half the registers.  Rows without vectors
+        // have zeros there, whose (0 - mean) rstd may be infinite, and NaN times dy = 0
+        const float scale = ONE || io.vectors ? rstd : 0.0f;
         const auto x_of = [&](int j, float (&x)[T::VEC]) {
             T::unpack(raw_h.v[j], x);
 #pragma unroll
-            for (int e = 0; e < T::VEC; e++) x[e] = (x[e] - mean) * rstd;  // of lanes without the vector: times dy = 0
+            for (int e = 0; e < T::VEC; e++) x[e] = (x[e] - mean) * scale;  // of lanes without the vector: times dy = 0
         };
-        const float xt = (T::widen(raw_h.t) - mean) * rstd;
+        const float xt = io.has_tail ? (T::widen(raw_h.t) - mean) * rstd : 0.0f;
         float s[2] = {0.0f, 0.0f};
         const auto one = [&](float xe, float de, float we, float& dwe, float& dbe) {
             const float g = de * we;

@@ -169,6 +169,29 @@ def test_layer_norm_far_from_zero(vrc):
     assert ((rstd[0].double() - rr[0]).abs() < 1e-2 * rr[0]).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("join,n", [("each", 2), ("sum", 2)])
+@pytest.mark.parametrize("width", [2, 4, 64])
+def test_layer_norm_grad_of_constant_rows_far_from_zero(vrc, width, join, n, dtype):
+    """h = 2^100 everywhere and rstd = 2^33: what lanes without a value compute in place of x,
+    (0 - mean) rstd, would be infinite, and NaN times their gradient of zero."""
+    f = gen(22)
+    x = [torch.full((3, width), 2.0**(100 if join == "each" else 99), dtype=dtype, device=DEV) for _ in range(n)]
+    w, dy = f(width).to(dtype), [f(3, width).to(dtype) for _ in range(n)]
+    y, h, mean, rstd = vrc.vrc_layer_norm(x, w, eps=2.0**-66, join=join)
+    assert all((t == 0).all() for t in y)
+    dx, dw, db = vrc.vrc_layer_norm_grad(dy, h, w, mean, rstd, join=join)
+    db_want, db_bound = 0, 0
+    for p, (hp, m, r) in enumerate(zip(listed(h), listed(mean), listed(rstd))):
+        assert (hp == 2.0**100).all() and (m == 2.0**100).all() and (r == 2.0**33).all()
+        rx, _, rb = ref.layer_norm_grad(dy if join == "sum" else [dy[p]], hp, w, m, r, None)
+        for q in range(n) if join == "sum" else [p]:
+            close(dx[q], rx, "dx")
+        db_want, db_bound = db_want + rb[0], db_bound + rb[1]
+    assert (dw == 0).all()
+    close(db, (db_want, db_bound), "dbias")
+
+
 @pytest.mark.parametrize("dtype", DT)
 def test_layer_norm_bad_rows_stay_alone(vrc, dtype):
     for width in (40, 1053, 9000, 40000):
