@@ -1067,7 +1067,8 @@ uint64_t tiles_of(const EntropyArgs& a, uint64_t rows, uint64_t cols, uint64_t b
 
 // The tile's side of a product of `tiles(b)` tiles of b x b: the smallest of which two a CU
 // are enough.  fp32's matrix instructions take so long that tiles of 128 feed them as well
-// as larger ones.
+// as larger ones, and those of 64 nearly so: where tiles of 128, half empty at the ends, are
+// more than a tenth more to compute, 64 are faster (515 x 35809 x 864 in 3, the gradients 957 -> 930 us).
 template <class T, class Tiles>
 int tile_side(Tiles tiles)
 {
