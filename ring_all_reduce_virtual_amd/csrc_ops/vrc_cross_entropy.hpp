@@ -472,6 +472,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64) void k_entropy(EntropyArgs a)
     } else {
         [[maybe_unused]] constexpr uint32_t PART = 32 * NI * 32;  // results of a wave on their way out
         if constexpr (OP == kGrad) {
+            if (KS > 1 && group) return;
             static_assert(WAVES * PART * T::ESZ <= S * STAGE, "the results' way out fits the ring");
             const uint32_t cols = a.piece[p].len - n0;
             Coef c[MI];
@@ -889,12 +890,19 @@ constexpr uint64_t kPackBytes = 1u << 30;    // packed weights of one piece: eno
 
 inline uint64_t up_to(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
+// What fp32 tiles take: rounds of one a CU, times what a tile of that kind takes.  A tile of 64
+// is a quarter of one of 128 and takes a twentieth more for its work, and a seventh where its
+// contraction is split.
+constexpr uint64_t kTile128 = 80, kTile64 = 21, kTile64Split = 23;
+inline uint64_t rounds(uint64_t tiles, uint64_t each) { return (tiles + kCus - 1) / kCus * each; }
+
 // What one call does, from its sizes and alignments alone, so that the workspace's
 // size can be asked for beforehand.
 template <class T>
 struct EntropyPlan {
     static constexpr uint64_t KT = kTileK<T>;
     bool few = false, stream = false; // tokens: up to kFewTokens, kStreamTokens
+    bool fine = false;                // LOGITS by the smallest tiles
     uint64_t parts = 1, rows = 0;     // of G's elements (few tokens); rows of DHIDDEN's sums, parts of `padded` each
     uint64_t vocab = 0, columns = 0;  // the whole; the same with each rank's rounded up to 256
     uint64_t padded, wide;            // tokens rounded up to 64; elements of a packed row
@@ -917,8 +925,10 @@ struct EntropyPlan {
     EntropyPlan(const EntropyCall& c, bool gradient)
     {
         pack_weight = false;
+        uint64_t along = 0;
         for (int r = 0; r < c.n; r++) {
             vocab += c.vocab[r];
+            along += (c.vocab[r] + 63) / 64;
             columns += up_to(c.vocab[r], 256);
             if (c.vocab[r]) pack_weight |= !direct(c.width, (uintptr_t)c.weight[r]);
         }
@@ -928,6 +938,7 @@ struct EntropyPlan {
         padded = few ? (c.tokens <= 32 ? 32 : c.tokens <= 64 ? 64 : 128) : up_to(c.tokens ? c.tokens : 1, 64);
         parts = few && T::ESZ == 2 ? 2 : 1;
         rows = few ? parts * padded : c.tokens;
+        fine = T::ESZ == 4 && !few && (c.tokens + 63) / 64 * along <= 2 * kCus;
         cut = c.width % KT != 0 && !pack_weight;
         // the gradient's hidden states are always packed: rows of tokens without gradient are zero
         pack_hidden = gradient ? true : c.width % KT != 0 || !direct(c.width, (uintptr_t)c.hidden);
@@ -938,7 +949,7 @@ struct EntropyPlan {
             tokens = c.tokens < 16384 ? c.tokens : 16384;
             if (pack_hidden) at_hidden = take(c.tokens * wide * T::ESZ);
             if (pack_weight) at_weight = take(piece * wide * T::ESZ);
-            at_stats = take(columns / (T::ESZ == 4 && tokens <= 64 ? 32 : 64) * tokens * sizeof(float2));
+            at_stats = take(columns / (T::ESZ == 4 && (tokens <= 64 || fine) ? 32 : 64) * tokens * sizeof(float2));
             at_picked = take(tokens * sizeof(float));
             return;
         }
@@ -956,12 +967,20 @@ struct EntropyPlan {
             // Few tiles: the contraction is split until each CU has one (256 x 256) or two,
             // of four tiles at least.
             const auto tiles = [&](uint64_t bm, uint64_t bn) { return ((rows + bm - 1) / bm) * ((c.width + bn - 1) / bn); };
+            const auto parts_of = [&](uint64_t bm, uint64_t bn) {
+                uint64_t s = (bm == 256 ? kCus : 2 * kCus) / tiles(bm, bn);
+                const uint64_t most = piece / KT / 4;
+                s = s < most ? s : most;
+                return s < 1 ? 1 : s > 128 ? 128 : s;
+            };
             if (!few) side = T::ESZ == 2 && tiles(256, 256) > 8 ? 256 : tiles(128, 128) > 8 ? 128 : 64;
+            if (T::ESZ == 4 && side == 128) {
+                const uint64_t t64 = tiles(64, 64), t128 = tiles(128, 128), s64 = parts_of(64, 64), s128 = parts_of(128, 128);
+                // 315 x 1915 x 5678: 108 us with its join and 89; 515 x 35809 x 864: 351 and 367
+                if (rounds(t64 * s64, kTile64Split) * s128 < rounds(t128 * s128, kTile128) * s64) side = 64;
+            }
             const uint64_t bm = few ? rows : side, bn = few ? (rows == 256 ? 256 : 128) : side;
-            uint64_t s = (bm == 256 ? kCus : 2 * kCus) / tiles(bm, bn);
-            const uint64_t most = piece / KT / 4;
-            s = s < most ? s : most;
-            splits = s < 1 ? 1 : s > 128 ? 128 : (int)s;
+            splits = (int)parts_of(bm, bn);
             sums = few || splits > 1 || pieces_of(piece) > 1;
             if (sums) at_sums = take((uint64_t)splits * rows * wide * sizeof(float));
         }
@@ -1066,14 +1085,14 @@ uint64_t tiles_of(const EntropyArgs& a, uint64_t rows, uint64_t cols, uint64_t b
 }
 
 // The tile's side of a product of `tiles(b)` tiles of b x b: the smallest of which two a CU
-// are enough.  fp32's matrix instructions take so long that tiles of 128 feed them as well
-// as larger ones, and those of 64 nearly so: where tiles of 128, half empty at the ends, are
-// more than a tenth more to compute, 64 are faster (515 x 35809 x 864 in 3, the gradients 957 -> 930 us).
+// are enough.  fp32's matrix instructions take so long that the rounds in which CUs compute
+// tiles decide (LOGITS of 900 x 9000 x 1000 in 7: 616 tiles of 128 273 us, 2,205 of 64 187;
+// 2048 x 8192 x 512: 1,024 of 128 150 us, 4,096 of 64 157).
 template <class T, class Tiles>
 int tile_side(Tiles tiles)
 {
+    if constexpr (T::ESZ == 4) return rounds(tiles(64), kTile64) < rounds(tiles(128), kTile128) ? 64 : 128;
     if (tiles(64) <= 2 * kCus) return 64;
-    if (T::ESZ == 4) return tiles(64) * 10 < tiles(128) * 36 ? 64 : 128;
     return tiles(128) <= 2 * kCus ? 128 : 256;
 }
 
@@ -1081,7 +1100,7 @@ int tile_side(Tiles tiles)
 template <class T, int OP>
 vrc_status_t launch_side(EntropyArgs& a, int side, uint64_t rows, uint64_t cols, bool cut, int splits, hipStream_t st)
 {
-    if (side == 64) return launch_entropy<T, OP, 64, 64, 2, 2, 4>(a, rows, cols, cut, splits, st);
+    if (side == 64) return launch_entropy<T, OP, 64, 64, 2, 2, T::ESZ == 4 ? 2 : 4>(a, rows, cols, cut, splits, st);
     if constexpr (T::ESZ == 2)
         if (side == 256) return launch_entropy<T, OP, 256, 256, 2, 4, 2>(a, rows, cols, cut, splits, st);
     return launch_entropy<T, OP, 128, 128, 2, 2, 2>(a, rows, cols, cut, splits, st);
@@ -1092,6 +1111,18 @@ vrc_status_t launch_tiles(EntropyArgs& a, uint64_t rows, uint64_t cols, bool cut
 {
     const int side = tile_side<T>([&](uint64_t b) { return tiles_of<OP>(a, rows, cols, b); });
     return launch_side<T, OP>(a, side, rows, cols, cut, 1, st);
+}
+
+// LOGITS.  fp32's are bound by the matrix instructions: up to two tiles of 64 a CU, of which some
+// CUs have twice as many as others, tiles of 32 by four waves that share the contraction are
+// faster (LOGITS of 315 x 1915 x 5678 in 7, 175 tiles, 127 -> 83 us; 2285 x 462 x 3231 in 5, 360,
+// 119 -> 90; 640 x 4096 x 1024, 640 tiles, 60 and 58, but 1024 tiles 78 and 89).
+template <class T, int OP>
+vrc_status_t launch_logits(EntropyArgs& a, uint64_t rows, bool fine, bool cut, hipStream_t st)
+{
+    if constexpr (T::ESZ == 4)
+        if (fine) return launch_entropy<T, OP, 32, 32, 1, 1, 4, 4>(a, rows, 0, cut, 1, st);
+    return launch_tiles<T, OP>(a, rows, 0, cut, st);
 }
 
 // Few rows (tokens): one tile has all of them, and its other side is as small as keeps two
@@ -1209,7 +1240,7 @@ vrc_status_t cross_entropy_typed(const EntropyCall& c, hipStream_t st)
             a.kwidth = (uint32_t)c.width;
             a.ktiles = (uint32_t)(plan.wide / plan.KT);
             const vrc_status_t rc = tokens <= 64 ? launch_few<T, kStats>(a, tokens, 0, plan.cut, 1, st)
-                                                 : launch_tiles<T, kStats>(a, tokens, 0, plan.cut, st);
+                                                 : launch_logits<T, kStats>(a, tokens, plan.fine, plan.cut, st);
             if (rc) return rc;
             tiles += a.tiles_n;
         }
@@ -1274,7 +1305,7 @@ vrc_status_t cross_entropy_grad_typed(const EntropyCall& c, hipStream_t st)
         a.out = g;
         a.pitch_out = plan.few ? plan.pitch_gt() : plan.pitch_g();
         rc = plan.few ? launch_few<T, kGradT>(a, plan.padded, 0, plan.cut, 1, st)
-                      : launch_tiles<T, kGrad>(a, plan.padded, 0, plan.cut, st);
+                      : launch_logits<T, kGrad>(a, plan.padded, plan.fine, plan.cut, st);
         if (rc) return rc;
         a.unscale = scale;
         a.a = g;

@@ -319,6 +319,15 @@ def test_larger_products(vrc, dtype, tokens, vocab, width):
     check_entropy_grad(vrc, tokens, vocab, width, DT[dtype])
 
 
+@pytest.mark.parametrize("tokens,vocab,width", [(65, [33, 1, 95], 36), (129, [31] * 16, 52), (315, [274] * 6 + [271], 180),
+                                                (513, [4100], 200), (640, [4096], 128), (1024, [2048], 33), (257, [120, 5, 129], 1030)])
+def test_fp32_products_of_each_tile(vrc, tokens, vocab, width):
+    """Few and many tiles for the CUs, of every side, with ends in each."""
+    say(f"{tokens} {vocab} {width}")
+    check_entropy(vrc, tokens, vocab, width, torch.float32)
+    check_entropy_grad(vrc, tokens, vocab, width, torch.float32)
+
+
 def test_layer_norm_past_32_bits(vrc):
     rows, width = (1 << 20) + 3, 4104  # 8.6 GB a tensor
     x = [torch.empty(rows, width, dtype=torch.bfloat16, device=DEV).normal_()]
