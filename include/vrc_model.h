@@ -130,8 +130,8 @@ vrc_status_t vrc_cross_entropy_workspace(const vrc_cross_entropy_t* ce, const vo
  * b = dloss[t] (0 where the target is ignore_index) and a = b + dlse[t], the
  * gradient of z_v is
  *     a exp(z_v - lse[t]) - b [v = target[t]],
- * exactly 0 for a token whose a and b are 0, whatever its hidden state and lse hold;
- * NaN in all of a token's with a target that is invalid as above.
+ * exactly 0 for a token whose a and b are 0, whatever its hidden state, lse and target
+ * hold; NaN in all of any other token's whose target is invalid as above.
  *   lse     as the forward call wrote it; dloss [tokens] of fp32; dlse the same, or NULL.
  *   dhidden [tokens, width], summed over the ranks, or NULL;
  *   dweight[r] [vocab[r], width], or dweight NULL.

@@ -689,7 +689,7 @@ __device__ __forceinline__ Coef coef_of(const TokenArgs& a, uint32_t t)
     Coef c;
     c.b = none ? 0.0f : dloss;
     c.a = c.b + dlse;
-    if (bad) c.a = __builtin_nanf("");
+    if (bad && (c.a != 0.0f || c.b != 0.0f)) c.a = __builtin_nanf("");  // without weight it has no gradient to spoil
     c.lse = a.lse[t];
     c.target = none || bad ? kNoTarget : (uint32_t)at;
     return c;

@@ -164,7 +164,9 @@ def vrc_cross_entropy_grad(hidden, weight, target, lse, dloss, dlse=None, ignore
     dhidden, like hidden, is summed over the ranks; dweight is one tensor per rank.
     ``need_hidden=False`` and ``need_weight=False`` (a frozen projection) leave one
     out, as None.  Tokens whose dloss (or target: ``ignore_index``) and dlse leave
-    nothing get zeros and add nothing to dweight, whatever their hidden states hold.
+    nothing get zeros and add nothing to dweight, whatever their hidden states and targets
+    hold.  Any other token whose target is outside the vocabulary makes its row of dhidden
+    and all of dweight NaN.
     ``recv``: (dhidden, list of dweight) to write to."""
     dhidden, dweight = (None, None) if recv is None else recv
     return _run(_native().cross_entropy_grad, "vrc_cross_entropy_grad", hidden, stream,

@@ -1,0 +1,49 @@
+"""The model's operators where their rules meet: tokens without weight whose targets are
+invalid, rows without values, shapes that hold as many elements, weights far apart, the
+precision of few tokens, and tensors too large for the caches or for 32-bit offsets.
+Tolerances are those of tests/model_reference.py."""
+import pytest
+import torch
+
+from tests import model_reference as ref
+from tests.test_gpu_model import (DEV, DT, IGNORE, check_norm, check_norm_grad, close, entropy_inputs, gen, say,  # noqa: F401
+                                  vrc)  # (vrc: the fixture)
+from tests.test_gpu_model_use import same
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# Targets outside the vocabulary
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("tokens", [5, 32, 70, 128, 200])
+def test_invalid_targets_without_weight_reach_nothing(vrc, dtype, tokens):
+    """A token whose dloss and dlse are 0 has no gradient, whatever its target, hidden state and
+    lse are: the bits are those of the same tokens ignored."""
+    say(f"{dtype} {tokens}")
+    hidden, weight, target = entropy_inputs(tokens, [130, 0, 60], 72, DT[dtype], 33, ignored=0.1)
+    _, lse = vrc.vrc_cross_entropy(hidden, weight, target)
+    dloss = torch.rand(tokens, device=DEV) + 0.1
+    gone = torch.arange(tokens, device=DEV) % 4 == 1
+    dloss[gone] = 0.0
+    dloss[1] = -0.0
+    stray = torch.tensor([-1, 190, 1 << 40, -(1 << 63), 1 << 31], device=DEV)
+    bad_target = torch.where(gone, stray[torch.arange(tokens, device=DEV) % 5], target)
+    bad_hidden, bad_lse = hidden.clone(), lse.clone()
+    bad_hidden[gone] = float("nan")
+    bad_lse[gone] = float("inf")
+    dlse = torch.rand(tokens, device=DEV) * ~gone
+    for second in (None, torch.zeros_like(dloss), dlse):
+        want = vrc.vrc_cross_entropy_grad(hidden, weight, torch.where(gone, torch.full_like(target, IGNORE), target), lse, dloss, dlse=second)
+        got = vrc.vrc_cross_entropy_grad(bad_hidden, weight, bad_target, bad_lse, dloss, dlse=second)
+        same(want, got, "as ignored")
+        assert not got[0][gone].any() and all(torch.isfinite(t).all() for t in got[1])
+    # one with any weight: NaN in all of its gradients, and the others' as before
+    for first, second in ((1.0, 0.0), (0.0, 1.0), (1.0, -1.0)):
+        one, two = dloss.clone(), torch.zeros_like(dloss)
+        one[1], two[1] = first, second
+        dh, dw = vrc.vrc_cross_entropy_grad(hidden, weight, bad_target, lse, one, dlse=two)
+        assert torch.isnan(dh[1]).all() and all(torch.isnan(t).all() for t in dw)
+        rest = torch.arange(tokens, device=DEV) != 1
+        assert torch.isfinite(dh[rest]).all() and not dh[gone & rest].any()
