@@ -59,7 +59,7 @@ typedef struct {
  *             computed from h before that rounding): the residual stream, and what
  *             the gradient takes.
  *   mean, rstd  NULL, or `parts` arrays of fp32, one value per row.  mean is NULL
- *             where not centred.
+ *             where not centred, both where rows have no values (width 0).
  * recv[r] may be send[r] itself (not for VRC_NORM_SCATTER), sum[p] may be
  * residual[p] itself; outputs overlap nothing else.  width < 2^26; rows of up to 16384
  * values are read once, longer ones once for each pass over them.

@@ -83,6 +83,7 @@ vrc_status_t layer_norm_impl(const vrc_layer_norm_t* d, const void* const* send,
     vrc_status_t rc = norm_call(d, n, &c, &dt);
     if (rc) return rc;
     if (mean && !c.center) return VRC_ERR_INVALID_ARG;
+    if (c.rows && c.width == 0 && (mean || rstd)) return VRC_ERR_INVALID_ARG;  // of rows without values there are none
     if (c.rows == 0 || c.width == 0) return VRC_OK;
     const uint64_t row = c.width * (uint64_t)esize(dt), wbytes = c.width * (uint64_t)(c.wide_weight ? 4 : esize(dt));
     Bufs<2 * kMaxRanks + 2> in;

@@ -120,7 +120,7 @@ def vrc_layer_norm(send, weight, bias=None, eps=1e-5, residual=None, join="each"
     ``weight`` and ``bias`` are of the rows' dtype or float32.  h is rounded from the
     fp32 values that y is computed from (without anything added, ``"each"`` returns
     ``send`` itself, or None where ``recv`` overwrites it); mean and rstd are float32, one per row, mean None where not
-    centred.  ``recv=send`` (not for ``"scatter"``) and ``sum=residual``, where h goes,
+    centred; rows need at least one value.  ``recv=send`` (not for ``"scatter"``) and ``sum=residual``, where h goes,
     run in place.  Gradient: ``vrc_layer_norm_grad``."""
     return _run(_native().layer_norm, "vrc_layer_norm", send, stream,
                 (send, weight, bias, eps, residual, _join(join), center, recv, sum))

@@ -47,3 +47,17 @@ def test_invalid_targets_without_weight_reach_nothing(vrc, dtype, tokens):
         assert torch.isnan(dh[1]).all() and all(torch.isnan(t).all() for t in dw)
         rest = torch.arange(tokens, device=DEV) != 1
         assert torch.isfinite(dh[rest]).all() and not dh[gone & rest].any()
+
+
+# ---------------------------------------------------------------------------
+# Sizes and shapes
+# ---------------------------------------------------------------------------
+def test_rows_without_values_are_refused(vrc):
+    """They have no mean and rstd to return."""
+    w = torch.ones(0, device=DEV)
+    for join in ("each", "sum", "scatter"):
+        for center in (True, False):
+            with pytest.raises(vrc.VrcError):
+                vrc.vrc_layer_norm([torch.ones(3, 0, device=DEV)] * 2, w, join=join, center=center)
+        y, h, mean, rstd = vrc.vrc_layer_norm([torch.ones(0, 0, device=DEV)] * 2, w, join=join)  # no rows either
+        assert all(t.shape == (0, 0) for t in y)
