@@ -8,6 +8,7 @@
 #include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <string>
 #include <vector>
 
 #include "vrc_model.h"
@@ -67,13 +68,20 @@ Like like(const at::Tensor& t, const char* where)
     return {type, t.device(), code};
 }
 
-// One contiguous tensor of a number of elements, type and device.
-const at::Tensor& same(PyObject* o, int64_t count, at::ScalarType type, const Like& l, const char* where, const char* what)
+std::string text(const Shape& s)
+{
+    std::string t = "[";
+    for (size_t i = 0; i < s.size(); i++) t += (i ? ", " : "") + std::to_string(s[i]);
+    return t + "]";
+}
+
+// One contiguous tensor of a shape, type and device.
+const at::Tensor& same(PyObject* o, const Shape& shape, at::ScalarType type, const Like& l, const char* where, const char* what)
 {
     const at::Tensor& t = tensor(o, where, what);
-    if (t.scalar_type() != type || t.numel() != count || t.device() != l.device || !t.is_contiguous()) {
-        PyErr_Format(PyExc_ValueError, "%s: %s must be contiguous, of %lld elements of the call's type, on the inputs' device", where,
-                     what, (long long)count);
+    if (t.scalar_type() != type || t.sizes() != at::IntArrayRef(shape) || t.device() != l.device || !t.is_contiguous()) {
+        PyErr_Format(PyExc_ValueError, "%s: %s must be contiguous %s of the call's type, on the inputs' device", where, what,
+                     text(shape).c_str());
         throw Set{};
     }
     return t;
@@ -118,7 +126,7 @@ void parts(PyObject* o, const std::vector<Shape>& shapes, at::ScalarType type, c
            const char* what, void** p)
 {
     if (one) {
-        p[0] = same(o, product(shapes[0]), type, l, where, what).data_ptr();
+        p[0] = same(o, shapes[0], type, l, where, what).data_ptr();
         return;
     }
     const Items items(o, where, what);
@@ -126,7 +134,7 @@ void parts(PyObject* o, const std::vector<Shape>& shapes, at::ScalarType type, c
         PyErr_Format(PyExc_ValueError, "%s: %s must be one tensor per rank", where, what);
         throw Set{};
     }
-    for (Py_ssize_t i = 0; i < items.n; i++) p[i] = same(items.at[i], product(shapes[i]), type, l, where, what).data_ptr();
+    for (Py_ssize_t i = 0; i < items.n; i++) p[i] = same(items.at[i], shapes[i], type, l, where, what).data_ptr();
 }
 
 PyObject* none()
@@ -293,7 +301,7 @@ const at::Tensor& norm_weight(PyObject* o, int64_t width, const Like& l, const c
     const at::Tensor& w = tensor(o, where, "weight");
     if (w.scalar_type() != l.type && w.scalar_type() != at::kFloat)
         fail(PyExc_TypeError, where, "weight must be of the rows' dtype or float32");
-    return same(o, width, w.scalar_type(), l, where, "weight");
+    return same(o, Shape{width}, w.scalar_type(), l, where, "weight");
 }
 
 vrc_layer_norm_t norm_of(const NormShapes& s, const Like& l, const at::Tensor& w, int join, bool center, double eps)
@@ -316,7 +324,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count)
         const Like l = like(*t0, where);
         const NormShapes s = norm_shapes(*t0, n, join, where);
         const at::Tensor& w = norm_weight(a[1], s.width, l, where);
-        const void* b = given(a[2]) ? same(a[2], s.width, w.scalar_type(), l, where, "bias").data_ptr() : nullptr;
+        const void* b = given(a[2]) ? same(a[2], Shape{s.width}, w.scalar_type(), l, where, "bias").data_ptr() : nullptr;
         const bool residual = given(a[4]), added = residual || join != VRC_NORM_EACH;
         if (residual) parts(a[4], s.parts, l.type, l, s.one, where, "residual", res);
         if (given(a[8]) && !added) refuse(where, "without a residual each rank's rows are their own sum");
@@ -401,10 +409,10 @@ Like entropy(PyObject* hidden, PyObject* weight, PyObject* target, PyObject* ign
     for (int r = 0; r < e->n; r++) {
         const at::Tensor& w = tensor(items.at[r], where, "every rank's weight");
         if (w.dim() != 2 || w.size(1) != width) refuse(where, "every rank's weight must be [rows of the vocabulary, hidden's width]");
-        same(items.at[r], w.numel(), l.type, l, where, "every rank's weight");
+        e->shapes.push_back({w.size(0), width});
+        same(items.at[r], e->shapes.back(), l.type, l, where, "every rank's weight");
         e->vocab[r] = (size_t)w.size(0);
         e->weight[r] = w.data_ptr();
-        e->shapes.push_back({w.size(0), width});
     }
     if (given(target)) {
         const at::Tensor& t = tensor(target, where, "target");
@@ -456,10 +464,9 @@ PyObject* cross_entropy_grad(PyObject*, PyObject* const* a, Py_ssize_t count)
         if (!given(a[2])) refuse(where, "target is missing");
         Entropy e;
         const Like l = entropy(a[0], a[1], a[2], a[6], where, &e);
-        const int64_t tokens = (int64_t)e.d.tokens;
-        const void* lse = same(a[3], tokens, at::kFloat, l, where, "lse").data_ptr();
-        const void* dloss = same(a[4], tokens, at::kFloat, l, where, "dloss").data_ptr();
-        const void* dlse = given(a[5]) ? same(a[5], tokens, at::kFloat, l, where, "dlse").data_ptr() : nullptr;
+        const void* lse = same(a[3], e.lead, at::kFloat, l, where, "lse").data_ptr();
+        const void* dloss = same(a[4], e.lead, at::kFloat, l, where, "dloss").data_ptr();
+        const void* dlse = given(a[5]) ? same(a[5], e.lead, at::kFloat, l, where, "dlse").data_ptr() : nullptr;
         const bool need_hidden = truth(a[7]), need_weight = truth(a[8]);
         const vrc_stream_t st = stream_of(a[11], l);
         size_t bytes = 0;

@@ -61,3 +61,32 @@ def test_rows_without_values_are_refused(vrc):
                 vrc.vrc_layer_norm([torch.ones(3, 0, device=DEV)] * 2, w, join=join, center=center)
         y, h, mean, rstd = vrc.vrc_layer_norm([torch.ones(0, 0, device=DEV)] * 2, w, join=join)  # no rows either
         assert all(t.shape == (0, 0) for t in y)
+
+
+def test_shapes_of_as_many_elements_are_refused(vrc):
+    """What is read or written row by row has the documented shape, not only its number of elements."""
+    f = gen(98)
+    x, w, b = [f(6, 4) for _ in range(2)], f(4), f(4)
+    y, h, mean, rstd = vrc.vrc_layer_norm(x, w, b, join="sum")
+    turned, wide = f(4, 6), f(3, 8)
+    for call in (
+            lambda: vrc.vrc_layer_norm(x, f(2, 2)), lambda: vrc.vrc_layer_norm(x, w, f(1, 4)), lambda: vrc.vrc_layer_norm(x, w, residual=[x[0], turned]),
+            lambda: vrc.vrc_layer_norm(x, w, residual=wide, join="sum"), lambda: vrc.vrc_layer_norm(x, w, recv=[turned, f(6, 4)]),
+            lambda: vrc.vrc_layer_norm(x, w, join="sum", sum=turned), lambda: vrc.vrc_layer_norm(x, w, join="sum", sum=f(24)),
+            lambda: vrc.vrc_layer_norm(x, w, residual=[f(4, 3), f(3, 4)], join="scatter"),
+            lambda: vrc.vrc_layer_norm_grad(x, turned, w, mean, rstd, join="sum"), lambda: vrc.vrc_layer_norm_grad(x, h, f(4, 1), mean, rstd, join="sum"),
+            lambda: vrc.vrc_layer_norm_grad(x, h, w, mean.view(2, 3), rstd, join="sum"), lambda: vrc.vrc_layer_norm_grad(x, h, w, mean, rstd.view(6, 1), join="sum"),
+            lambda: vrc.vrc_layer_norm_grad(x, h, w, mean, rstd, dh=wide, join="sum"), lambda: vrc.vrc_layer_norm_grad(x, h, w, mean, rstd, join="sum", recv=[f(6, 4), turned])):
+        with pytest.raises(ValueError):
+            call()
+    hidden, weight, target = f(2, 3, 8), [f(5, 8), f(4, 8)], torch.zeros(2, 3, dtype=torch.int64, device=DEV)
+    loss, lse = vrc.vrc_cross_entropy(hidden, weight, target)
+    for call in (
+            lambda: vrc.vrc_cross_entropy_grad(hidden, weight, target, lse.view(6), loss), lambda: vrc.vrc_cross_entropy_grad(hidden, weight, target, lse, loss.view(3, 2)),
+            lambda: vrc.vrc_cross_entropy_grad(hidden, weight, target, lse, loss, dlse=loss.view(6)),
+            lambda: vrc.vrc_cross_entropy_grad(hidden, weight, target, lse, loss, recv=(f(6, 8), None)),
+            lambda: vrc.vrc_cross_entropy_grad(hidden, weight, target, lse, loss, recv=(None, [f(8, 5), f(4, 8)]))):
+        with pytest.raises(ValueError):
+            call()
+    dh, dw = vrc.vrc_cross_entropy_grad(hidden, weight, target, lse, loss, dlse=loss)
+    assert dh.shape == (2, 3, 8) and [t.shape for t in dw] == [(5, 8), (4, 8)]
