@@ -1080,8 +1080,7 @@ uint64_t tiles_of(const EntropyArgs& a, uint64_t rows, uint64_t cols, uint64_t b
     uint64_t along = 0;
     for (int i = 0; i < a.pieces; i++) along += (a.piece[i].len + b - 1) / b;
     if constexpr (OP == kStats || OP == kGrad) return (rows + b - 1) / b * along;
-    else if constexpr (OP == kDweight || OP == kDweightT) return (cols + b - 1) / b * along;
-    else return ((rows + b - 1) / b) * ((cols + b - 1) / b);
+    else return (cols + b - 1) / b * along;
 }
 
 // The tile's side of a product of `tiles(b)` tiles of b x b: the smallest of which two a CU

@@ -25,7 +25,6 @@
 namespace vrc {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAlong = 0, kAcross = 1;
@@ -85,7 +84,7 @@ __device__ __forceinline__ void read_across(const uint32_t (&at)[F], u32x4 (&out
 {
     u32x2 a[F], b[F];
 #define VRC_TR(d, s, o) "ds_read_b64_tr_b16 %" #d ", %" #s " offset:%" #o "\n\t"
-    static_assert(F == 1 || F == 2 || F == 3 || F == 4 || F == 6, "operands of a wave");
+    static_assert(F == 1 || F == 2 || F == 4 || F == 6, "operands of a wave");
     if constexpr (F == 1) {
         __asm__ volatile(VRC_TR(0, 2, 3) VRC_TR(1, 2, 4) "s_waitcnt lgkmcnt(0)"
                          : "=&v"(a[0]), "=&v"(b[0]) : "v"(at[0]), "n"(OFF), "n"(OFF + STEP) : "memory");
@@ -93,11 +92,6 @@ __device__ __forceinline__ void read_across(const uint32_t (&at)[F], u32x4 (&out
         __asm__ volatile(VRC_TR(0, 4, 6) VRC_TR(1, 4, 7) VRC_TR(2, 5, 6) VRC_TR(3, 5, 7) "s_waitcnt lgkmcnt(0)"
                          : "=&v"(a[0]), "=&v"(b[0]), "=&v"(a[1]), "=&v"(b[1])
                          : "v"(at[0]), "v"(at[1]), "n"(OFF), "n"(OFF + STEP) : "memory");
-    } else if constexpr (F == 3) {
-        __asm__ volatile(VRC_TR(0, 6, 9) VRC_TR(1, 6, 10) VRC_TR(2, 7, 9) VRC_TR(3, 7, 10) VRC_TR(4, 8, 9) VRC_TR(5, 8, 10)
-                         "s_waitcnt lgkmcnt(0)"
-                         : "=&v"(a[0]), "=&v"(b[0]), "=&v"(a[1]), "=&v"(b[1]), "=&v"(a[2]), "=&v"(b[2])
-                         : "v"(at[0]), "v"(at[1]), "v"(at[2]), "n"(OFF), "n"(OFF + STEP) : "memory");
     } else if constexpr (F == 4) {
         __asm__ volatile(VRC_TR(0, 8, 12) VRC_TR(1, 8, 13) VRC_TR(2, 9, 12) VRC_TR(3, 9, 13) VRC_TR(4, 10, 12) VRC_TR(5, 10, 13)
                          VRC_TR(6, 11, 12) VRC_TR(7, 11, 13) "s_waitcnt lgkmcnt(0)"
