@@ -90,3 +90,153 @@ def test_shapes_of_as_many_elements_are_refused(vrc):
             call()
     dh, dw = vrc.vrc_cross_entropy_grad(hidden, weight, target, lse, loss, dlse=loss)
     assert dh.shape == (2, 3, 8) and [t.shape for t in dw] == [(5, 8), (4, 8)]
+
+
+# ---------------------------------------------------------------------------
+# The gradients of the logits, G, between the products
+# ---------------------------------------------------------------------------
+def grad_inputs(tokens, dtype, seed):
+    hidden, weight, target = entropy_inputs(tokens, [700, 0, 333], 192, dtype, seed, ignored=0.1)
+    target[0] = 699
+    z, _ = ref.logits(hidden, weight)
+    return hidden, weight, target, z, torch.logsumexp(z, 1).float()
+
+
+def logit_grads(z, target, lse, dloss):
+    """G in 64 bits, and the largest |a| or |b|, in whose units it is held."""
+    b = torch.where(target != IGNORE, dloss, torch.zeros_like(dloss)).double()
+    g = (z - lse.double()[:, None]).exp() * b[:, None]
+    rows = torch.nonzero(target != IGNORE)[:, 0]
+    g[rows, target[rows]] -= b[rows]
+    return g, float(b.abs().max())
+
+
+def bounds(hidden, weight, target, lse, dloss, of_g):
+    """((dhidden, bound), [(dweight, bound)]) where G is off by at most `of_g` (element by element) from its rounding."""
+    (dh, edh), dw = ref.cross_entropy_grad(hidden, weight, target, lse, dloss, None, IGNORE, torch.float32)
+    w, h = torch.cat(weight).double().abs(), hidden.double().abs()
+    more = (of_g.t() @ h).split([x.shape[0] for x in weight])
+    return (dh, edh + of_g @ w), [(d, e + m) for (d, e), m in zip(dw, more)]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 7, 32, 33, 64, 128])
+def test_few_tokens_hold_two_values_of_each(vrc, dtype, tokens):
+    """Up to 128 tokens of 16-bit types G is its rounding and the rounding of what that left: off by at most
+    half a step of half a step of the type (and fp16's subnormals, in units of 2^-14 of the largest)."""
+    dtype = DT[dtype]
+    hidden, weight, target, z, lse = grad_inputs(tokens, dtype, 35)
+    f = gen(36)
+    dloss = f(tokens) + 0.3
+    g, most = logit_grads(z, target, lse, dloss)
+    half = ref.EPS_HALF[dtype]
+    least = 2.0**-25 * 2.0**-14 * most if dtype is torch.float16 else 0.0
+    want_h, want_w = bounds(hidden, weight, target, lse, dloss, g.abs() * half * half + least * (g != 0))
+    dh, dw = vrc.vrc_cross_entropy_grad(hidden, weight, target, lse, dloss)
+    close(dh, want_h, (tokens, "dhidden"))
+    for got, want in zip(dw, want_w):
+        close(got, want, (tokens, "dweight"))
+    # one value of each would not pass: the bound tells the two apart
+    unit = most * (2.0**-14 if dtype is torch.float16 else 1.0)
+    once = ((g / unit).to(dtype).double() * unit).t() @ torch.where(dloss[:, None] != 0, hidden.double(), 0.0)
+    with pytest.raises(AssertionError):
+        close(once[:700].to(dtype), want_w[0], "once")
+
+
+@pytest.mark.parametrize("tokens", [40, 200])
+def test_weights_far_apart_in_fp16(vrc, tokens):
+    """One unit holds all tokens' G: elements from 2^-28 of the largest weight on keep all bits of fp16, smaller ones
+    are rounded to multiples of 2^-38 of it."""
+    hidden, weight, target, z, lse = grad_inputs(tokens, torch.float16, 37)
+    dloss = 1024.0 * 2.0 ** -(torch.arange(tokens, device=DEV) % 31).float()
+    g, most = logit_grads(z, target, lse, dloss)
+    assert most == 1024.0
+    of_g = torch.where(g.abs() >= 2.0**-28 * most, g.abs() * 2.0**-11, torch.full_like(g, 2.0**-39 * most)) * (g != 0)
+    want_h, want_w = bounds(hidden, weight, target, lse, dloss, of_g)
+    dh, dw = vrc.vrc_cross_entropy_grad(hidden, weight, target, lse, dloss)
+    close(dh, want_h, (tokens, "dhidden"))
+    for got, want in zip(dw, want_w):
+        close(got, want, (tokens, "dweight"))
+
+
+# ---------------------------------------------------------------------------
+# Large tensors
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("join,n,vectors", [("sum", 2, 60.3), ("scatter", 3, 128), ("sum", 3, 250.2), ("scatter", 2, 512), ("sum", 4, 1000.7), ("scatter", 3, 2048),
+                                            ("sum", 16, 2040.2)])
+def test_rows_that_pass_by_the_caches(vrc, join, n, vectors, dtype):
+    """256 MiB and more, of several sources, for each kind of row: narrow and wide, with and without elements behind
+    the last vector, many rows and few."""
+    dtype = DT[dtype]
+    size = torch.finfo(dtype).bits // 8
+    width = int(vectors * (16 // size))
+    rows = -(-(256 << 20) // (width * n * size)) + 1
+    say(f"{join} {n} {dtype} {rows} x {width}")
+    check_norm(vrc, join, n, rows, width, dtype, residual=n == 3)
+    torch.cuda.empty_cache()
+    check_norm_grad(vrc, join, n, rows, width, dtype, residual=n == 3)
+    torch.cuda.empty_cache()
+
+
+def test_layer_norm_weights_past_32_bits(vrc):
+    """All gradients of 8.6 GB of rows of which twelve, around the places where 32-bit offsets end, have any."""
+    rows, width = (1 << 20) + 3, 4104
+    x = torch.empty(rows, width, dtype=torch.bfloat16, device=DEV).normal_()
+    w = gen(5)(width).bfloat16()
+    _, _, mean, rstd = vrc.vrc_layer_norm([x], w)
+    pick = torch.tensor([0, 1, 261632, 261633, 523263, 523264, 523265, 523266, 784896, 784897, rows - 2, rows - 1], device=DEV)
+    dy = torch.zeros_like(x)
+    dy[pick] = gen(6)(12, width).bfloat16()
+    dx, dw, db = vrc.vrc_layer_norm_grad([dy], [x], w, mean, rstd)
+    rx, rw, rb = ref.layer_norm_grad([dy[pick]], x[pick], w, mean[0][pick], rstd[0][pick], None)
+    close(dw, rw, "dweight")
+    close(db, rb, "dbias")
+    close(dx[0][pick], rx, "dx")
+    dx[0][pick] = 0
+    assert not dx[0].any()
+
+
+def test_cross_entropy_gradients_past_32_bits(vrc):
+    """Both gradients of 4.6 GB of weights, whole.  The hidden states have 16 values, so that a logit's bound
+    counts as many products; some rows, on both sides of 4 GiB, have an eighth of the probability."""
+    tokens, width, vocab = 3, 16384, 140001
+    f = gen(7)
+    cols = torch.randperm(width, device=DEV)[:16]
+    hidden = torch.zeros(tokens, width, device=DEV)
+    hidden[:, cols] = f(tokens, 16) / 8  # logits of about half around 0, and 12 for the likely rows
+    hidden[:, cols[0]] = 1.0
+    hidden = hidden.bfloat16()
+    weight = [f(5, width).bfloat16(), torch.empty(vocab, width, dtype=torch.bfloat16, device=DEV).normal_()]
+    likely = torch.tensor([0, 65536, 131071, 131072, 131073, vocab - 2, vocab - 1], device=DEV)
+    weight[1][likely, cols[0]] = 12.0
+    target = torch.tensor([vocab + 4, 5 + 131072, 3], device=DEV)
+
+    def chunks():
+        at = 0
+        for r, w in enumerate(weight):
+            for i in range(0, w.shape[0], 10000):
+                yield at, r, i, w[i:i + 10000].double()
+                at += min(10000, w.shape[0] - i)
+
+    h = hidden.double()
+    z = torch.cat([h @ c.t() for _, _, _, c in chunks()], 1)
+    ez = torch.cat([17 * ref.U * (h.abs() @ c.abs().t()) for _, _, _, c in chunks()], 1)
+    lse, dloss = torch.logsumexp(z, 1).float(), f(tokens)
+    dh, dw = vrc.vrc_cross_entropy_grad(hidden, weight, target, lse, dloss)
+    off = z - lse.double()[:, None]
+    p = off.exp() * dloss.double()[:, None]
+    g = p.clone()
+    g[torch.arange(tokens, device=DEV), target] -= dloss.double()
+    eg = p.abs() * (ez + 4 * ref.U * (1 + off.abs()) + 2 * ref.U) + 4 * ref.U * (p.abs() + g.abs()) + g.abs() * 2.0**-16
+    want, bound, size = torch.zeros_like(h), torch.zeros_like(h), torch.zeros_like(h)
+    for at, r, i, c in chunks():
+        a, b = at, at + c.shape[0]
+        want += g[:, a:b] @ c
+        bound += eg[:, a:b] @ c.abs()
+        size += g[:, a:b].abs() @ c.abs()
+        close(dw[r][i:i + 10000], (g[:, a:b].t() @ h, eg[:, a:b].t() @ h.abs() + (tokens + 4) * ref.U * (g[:, a:b].abs().t() @ h.abs())), ("dweight", r, i))
+    bound += (vocab + 160) * ref.U * size
+    # a likely row's part (its G times a mean absolute value of 0.8) is well above what the sums' order may change
+    assert (4 * bound.mean(1) < 0.8 * g[:, 5 + likely].abs().min(1).values).all()
+    close(dh, (want, bound), "dhidden")
