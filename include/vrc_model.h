@@ -135,10 +135,14 @@ vrc_status_t vrc_cross_entropy_workspace(const vrc_cross_entropy_t* ce, const vo
  *   lse     as the forward call wrote it; dloss [tokens] of fp32; dlse the same, or NULL.
  *   dhidden [tokens, width], summed over the ranks, or NULL;
  *   dweight[r] [vocab[r], width], or dweight NULL.
- * The gradients of the logits are rounded to `dtype` (scaled by the largest |a| or
- * |b|, so that fp16's range does not matter) before the two products that are made
- * of them, whose sums are held in fp32 and rounded once.  Outputs overlap nothing
- * else.  Sums are taken in a fixed order: equal calls on one device give equal bits.
+ * The gradients of the logits are rounded to `dtype` before the two products that
+ * are made of them, whose sums are held in fp32 and rounded once; of up to 128 tokens
+ * of a 16-bit type they are held as two such values, the rounding and what it left.
+ * They are held in units of the largest |a| or |b| of the call's tokens, so that the
+ * loss's scale does not matter.  fp16's, in one value as in two, lose bits below 2^-28
+ * of it and are 0 below 2^-39 of it: of a token that weighs 2^-k of the largest, those
+ * of probabilities below 2^(k - 28) and 2^(k - 39).  Outputs overlap nothing else.  Sums
+ * are taken in a fixed order: equal calls on one device give equal bits.
  */
 vrc_status_t vrc_cross_entropy_grad(const vrc_cross_entropy_t* ce, const void* hidden, const void* const* weight,
                                     const long long* target, const float* lse, const float* dloss, const float* dlse,

@@ -14,11 +14,19 @@
 // G is the only thing kept, [tokens, a piece's columns]; DHIDDEN reads it along its
 // rows, DWEIGHT across them.
 //
-// Few tokens (kFewTokens at most) are bound by the weights' bytes and their gradients'.
-// There G is held as its transpose, a row of the vocabulary a row, and, of 16-bit types, as
-// two values each, G rounded and what that left: the matrix cores have the time, and the
-// rounding of a few large elements of G does not average out as it does over many tokens
-// (7 tokens: errors of the weights' gradients 0.0028 of their norm, bf16's own rounding 0.0017).
+// G of 16-bit types is rounded to the type, for the matrix cores.  However many tokens there are,
+// a row of either gradient is mostly one element of G, the target's, so that the error of one value
+// of each adds to that of the output's rounding: where tokens weigh differently, errors are 0.0022
+// of the norm in bf16 (the output's rounding alone 0.0017) and 0.00028 (0.00021) in fp16, for 129
+// tokens and for 4096; of a mean over tokens of small probability, whose elements of G are close
+// to the unit, 0.0017 and 0.00021.
+// Few tokens (kFewTokens at most) are bound by the weights' bytes and their gradients'.  There G is held
+// as its transpose, a row of the vocabulary a row, and, of 16-bit types, as two values each, G rounded and
+// what that left, which keeps errors at the output's rounding (7 tokens 0.0017, with one value 0.0028).
+// It is a choice by what it costs, 65536 x 4096 bf16 with two values and (by the other kernels) with one:
+// 33 tokens 402 us and 367, 64 404 and 375, 96 508 and 405, 128 534 and 432; 128 tokens of 8000 x 1024
+// 59 and 37.  Where the matrix instructions bound, it would be two of three products made twice (4096
+// tokens: some 9,000 us for 5,369).
 //
 // Measured on MI355X, 4096 tokens and 8 x (8192 x 4096) bf16, calls one after the other on other
 // inputs: the loss 1,732 us (1.27 PFLOP/s, matrix pipes busy for 70 % of all cycles), the gradients
@@ -705,8 +713,11 @@ __device__ __forceinline__ bool live(const TokenArgs& a, uint32_t t)
 
 // The tokens' coefficients, by one workgroup.  16-bit G is held in units of the largest
 // |a| or |b| (fp16: 2^-14 of it): the targets' elements of a loss whose tokens weigh
-// the same are then rounded from 1 - p instead of from an arbitrary weight, and fp16's
-// small range does not matter.  scale[0]: one such unit.
+// the same are then rounded from 1 - p instead of from an arbitrary weight, and the loss's
+// scale does not matter.  fp16 then keeps all bits of elements from 2^-28 of the largest on; smaller
+// ones are multiples of 2^-38 of it.  A unit for each token would save those of tokens that weigh little
+// from one product, by the hidden states' rows, and lose as much in the other, whose sum is over
+// tokens.  scale[0]: one such unit.
 template <class T>
 __device__ __forceinline__ void write_coefs(const TokenArgs& a, Coef* coef, float* scale, float* lds)
 {

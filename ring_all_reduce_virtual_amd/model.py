@@ -166,7 +166,9 @@ def vrc_cross_entropy_grad(hidden, weight, target, lse, dloss, dlse=None, ignore
     out, as None.  Tokens whose dloss (or target: ``ignore_index``) and dlse leave
     nothing get zeros and add nothing to dweight, whatever their hidden states and targets
     hold.  Any other token whose target is outside the vocabulary makes its row of dhidden
-    and all of dweight NaN.
+    and all of dweight NaN.  16-bit types round the gradients of the logits on the way, fp16
+    in one range for the whole call: include/vrc_model.h has what that keeps of tokens that
+    weigh little.
     ``recv``: (dhidden, list of dweight) to write to."""
     dhidden, dweight = (None, None) if recv is None else recv
     return _run(_native().cross_entropy_grad, "vrc_cross_entropy_grad", hidden, stream,
