@@ -652,7 +652,8 @@ __device__ __forceinline__ float2 join_sums(float2 p, float2 q)
 // The tiles' maxima and sums of each token, joined: RUNS lanes have a token, whose tiles
 // they take in turn.  16 lanes, so that neighbouring ones read neighbouring tokens;
 // where tokens are few 256, as a lane's tiles follow one another at memory's latency (one
-// token's 512 tiles: 17 us with 16 lanes, 4 us with 256).
+// token's 512 tiles: 17 us with 16 lanes, 4 us with 256; a loss over 65536 of width 64 of 64 tokens 20.0
+// and 9.7, 1,024 39.8 and 37.7, 2,048 68.2 and 71.6).
 template <int RUNS>
 __global__ __launch_bounds__(256) void k_entropy_loss(const float2* stats, const float* picked, uint32_t tiles, uint32_t tokens,
                                                       const long long* target, long long ignore, uint32_t vocab, float* loss,
@@ -844,8 +845,9 @@ __global__ __launch_bounds__(1024) void k_entropy_prepare(TokenArgs a, const cha
 
 // out = unscale x the sums of every split and, in it, of every part (few tokens: of G
 // rounded and of what that left), rounded: in their order within each of RUNS interleaved
-// runs and then of the runs.  16 runs where there are many sums of few values, which one
-// lane would fetch one after the other (3 tokens of 17 values, 109 splits: 27 us).
+// runs and then of the runs.  16 runs where there are many sums (eight and more), which one
+// lane would fetch one after the other (3 tokens of 17 values, 109 splits: 27 us; the gradient by hidden
+// states of 33 tokens, 4000 x 512, 24.5 us with one run and 22.6 with 16, of 300, 65536 x 1024, 155.8 and 157.4).
 template <class T, int RUNS>
 __global__ __launch_bounds__(256) void k_entropy_join(const float* sums, uint32_t count, uint32_t rows, uint32_t tokens,
                                                       uint32_t width, uint32_t pitch, const float* unscale, char* out)
@@ -984,6 +986,11 @@ struct EntropyPlan {
                 s = s < most ? s : most;
                 return s < 1 ? 1 : s > 128 ? 128 : s;
             };
+            // Sides of 16-bit types, us with 64, 128 and 256 (the hidden states' gradient alone): 200 x 16384 x 512,
+            // 8 tiles of 128, 39, 40, 40; 200 x 65536 x 1024, 16 of 128, 136, 119, 108.  128 and 256 are within a
+            // tenth of each other from 8 to 32 tiles of 256, as the contraction is split over all CUs in any case:
+            // 8 tiles, 500 x 16384 x 1024, 67, 67, 73, but 500 x 65536 x 1024 238, 193, 173; 16 tiles, 1024 x 65536
+            // x 1024, 440, 338, 298; 32 tiles, 300 x 65536 x 4096, 782, 462, 484.
             if (!few) side = T::ESZ == 2 && tiles(256, 256) > 8 ? 256 : tiles(128, 128) > 8 ? 128 : 64;
             if (T::ESZ == 4 && side == 128) {
                 const uint64_t t64 = tiles(64, 64), t128 = tiles(128, 128), s64 = parts_of(64, 64), s128 = parts_of(128, 128);
@@ -1095,7 +1102,11 @@ uint64_t tiles_of(const EntropyArgs& a, uint64_t rows, uint64_t cols, uint64_t b
 }
 
 // The tile's side of a product of `tiles(b)` tiles of b x b: the smallest of which two a CU
-// are enough.  fp32's matrix instructions take so long that the rounds in which CUs compute
+// are enough (bf16, LOGITS with its join, us with sides of 64, 128 and 256: 80 x 8192 x 1024, 256 tiles of
+// 64, 13.6, 19.9, 30.6; 500 x 4096 x 2048, 512 of 64, 20.4, 28.2, 47.6; 80 x 65536 x 4096, 512 of 128, 155,
+// 111, 127; 1024 x 8192 x 1024, 512 of 128, 37, 26, 31; 200 x 65536 x 4096, 1,024 of 128, 239, 154, 126;
+// 300 x 65536 x 4096, 1,536 of 128, 353, 214, 212; the gradients, whose LOGITS and DWEIGHT go by it, of
+// 1024 x 8192 x 1024 115, 93, 106, of 1024 x 16384 x 1024 206, 145, 130).  fp32's matrix instructions take so long that the rounds in which CUs compute
 // tiles decide (LOGITS of 900 x 9000 x 1000 in 7: 616 tiles of 128 273 us, 2,205 of 64 187;
 // 2048 x 8192 x 512: 1,024 of 128 150 us, 4,096 of 64 157).
 template <class T, class Tiles>

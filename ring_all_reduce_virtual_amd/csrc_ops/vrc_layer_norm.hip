@@ -588,6 +588,10 @@ vrc_status_t norm_typed(const NormCall& c, hipStream_t st)
 {
     const NormArgs a = args_of<T>(c);
     const uint64_t v = row_vectors<T>(c.width), rows = most_rows(c);
+    // Few rows have four times as many lanes each (256 in place of 64, 1024 in place of 256).  4 ranks' bf16 rows summed with a residual, us with those and with the others: width 1000, 16 rows 4.4
+    // and 4.9, 512 5.8 and 6.4, 2,048 12.1 and 10.0; 2048, 16 rows 4.4 and 6.1, 512 7.3 and 8.9, 2,048 17.1 and 15.8;
+    // 8192, 16 rows 5.7 and 6.5, 256 10.3 and 11.1, 384 15.6 and 12.8.  One limit for every width is a compromise:
+    // rows of 257 to 512 vectors gain nothing (4096, 16 rows 5.5 and 5.1, 256 8.2 and 8.3, 384 12.3 and 9.2).
     const bool few = rows * (uint64_t)c.parts < 512;
 #define VRC_NORM(LANES, V) return launch_norm<T, LANES, V>(a, rows, c.parts, streams(c, T::ESZ), st)
     if (v <= 64) VRC_NORM(64, 1);
@@ -635,7 +639,7 @@ vrc_status_t norm_grad_rows(const NormCall& c, const NormArgs& a, unsigned group
     const uint64_t v = row_vectors<T>(c.width);
 #define VRC_NORM(LANES, V) return launch_norm_grad<T, LANES, V>(a, groups, c.parts, streams(c, T::ESZ), st)
     if (v <= 64) VRC_NORM(64, 1);
-    if (v <= 128) VRC_NORM(64, 2);
+    if (v <= 128) VRC_NORM(64, 2);  // 4 x [2056, 1000] fp16, summed, 14.6 us; 17.5 with 256 lanes a row
     if (v <= 256) VRC_NORM(256, 1);
     if (v <= 512) VRC_NORM(256, 2);
     if (v <= 1024) VRC_NORM(512, 2);
