@@ -26,12 +26,12 @@
 // It is a choice by what it costs, 65536 x 4096 bf16 with two values and (by the other kernels) with one:
 // 33 tokens 402 us and 367, 64 404 and 375, 96 508 and 405, 128 534 and 432; 128 tokens of 8000 x 1024
 // 59 and 37.  Where the matrix instructions bound, it would be two of three products made twice (4096
-// tokens: some 9,000 us for 5,369).
+// tokens: some 9,000 us for 5,400).
 //
 // Measured on MI355X, 4096 tokens and 8 x (8192 x 4096) bf16, calls one after the other on other
-// inputs: the loss 1,732 us (1.27 PFLOP/s, matrix pipes busy for 70 % of all cycles), the gradients
-// 5,369 us (1.23 PFLOP/s: for each of four pieces LOGITS 448, DHIDDEN 460, DWEIGHT 435 us).
-// One token 106 us for 537 MB; the gradients of 7 tokens, 8 x (4096 x 4096), 171 us (LOGITS 57,
+// inputs: the loss 1,732 us (1.27 PFLOP/s, matrix pipes busy for 71 % of all cycles), the gradients
+// 5,369 to 5,548 us (1.19 to 1.23 PFLOP/s: for each of four pieces LOGITS 437, DHIDDEN 466, DWEIGHT 435
+// us).  One token 107 us for 537 MB; the gradients of 7 tokens, 8 x (4096 x 4096), 171 us (LOGITS 58,
 // DHIDDEN 53, DWEIGHT 51).  fp32, 2048 x 16384 x 2048: 138 TFLOP/s.
 #pragma once
 

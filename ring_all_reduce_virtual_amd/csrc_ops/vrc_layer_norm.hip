@@ -9,8 +9,8 @@
 // squares of the differences from it), not one over sums of squares, which
 // loses the variance of rows far from zero.
 //
-// Measured on MI355X: 8 x [8192, 4096] bf16, summed with the residual, eight outputs, 224 us
-// (5.4 TB/s; a large copy 4.9); the gradient of 8 x [2048, 8192] bf16 203 us and 7 us for the
+// Measured on MI355X: 8 x [8192, 4096] bf16, summed with the residual, eight outputs, 225 us
+// (5.4 TB/s; a large copy 4.9); the gradient of 8 x [2048, 8192] bf16 204 us and 7 us for the
 // join of 512 partial sums; 3 x [4003, 1053] fp32, scattered, 20 us (5.0 TB/s).
 #include <hip/hip_runtime.h>
 
