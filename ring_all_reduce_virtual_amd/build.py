@@ -81,12 +81,16 @@ BINDING_SRC = os.path.join(CSRC_OPS, "vrc_model_binding.cpp")
 BINDING_LIB = os.path.join(PKG, "_vrc_model.so")
 
 
-def build_binding(verbose: bool = False) -> str:
+def build_binding(verbose: bool = False) -> str | None:
     """Build the compiled Python binding of include/vrc_model.h against torch's
-    headers and libvrc_ops.so (host code only)."""
+    headers and libvrc_ops.so (host code only).  Without torch, whose tensors it takes,
+    there is none: the libraries serve callers of their C ABI."""
     import sysconfig
 
     spec = importlib.util.find_spec("torch")
+    if spec is None:
+        print("torch is not installed: the model operators' Python binding is not built", flush=True)
+        return None
     torch = os.path.dirname(spec.origin)
     tmp = BINDING_LIB + ".tmp"
     system = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
