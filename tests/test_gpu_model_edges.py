@@ -2,13 +2,15 @@
 invalid, rows without values, shapes that hold as many elements, weights far apart, the
 precision of few tokens, and tensors too large for the caches or for 32-bit offsets.
 Tolerances are those of tests/model_reference.py."""
+import threading
+
 import pytest
 import torch
 
 from tests import model_reference as ref
-from tests.test_gpu_model import (DEV, DT, IGNORE, check_norm, check_norm_grad, close, entropy_inputs, gen, say,  # noqa: F401
-                                  vrc)  # (vrc: the fixture)
-from tests.test_gpu_model_use import same
+from tests.test_gpu_model import (DEV, DT, IGNORE, check_entropy, check_entropy_grad, check_norm, check_norm_grad, close,
+                                  entropy_inputs, gen, say, vrc)  # noqa: F401  (vrc: the fixture)
+from tests.test_gpu_model_use import inputs, passes, same
 
 pytestmark = pytest.mark.gpu
 
@@ -244,3 +246,74 @@ def test_cross_entropy_gradients_past_32_bits(vrc):
     # a likely row's part (its G times a mean absolute value of 0.8) is well above what the sums' order may change
     assert (4 * bound.mean(1) < 0.8 * g[:, 5 + likely].abs().min(1).values).all()
     close(dh, (want, bound), "dhidden")
+
+
+# ---------------------------------------------------------------------------
+# The largest sizes, and calls at once
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", DT)
+def test_norms_of_more_rows_than_one_turn_has(vrc, dtype):
+    """Five million rows, which the largest grid takes in two turns."""
+    for width in (3, 16):
+        check_norm(vrc, "each", 1, (5 << 20) + 3, width, DT[dtype])
+        check_norm_grad(vrc, "each", 1, (5 << 20) + 3, width, DT[dtype])
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_norms_of_the_widest_rows(vrc, dtype):
+    check_norm(vrc, "sum", 2, 1, (1 << 26) - 1, DT[dtype])
+    check_norm_grad(vrc, "sum", 2, 1, (1 << 26) - 1, DT[dtype])
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("tokens,width", [(3, (1 << 20) - 1), (40, (1 << 20) - 64), (200, (1 << 20) - 1)])
+def test_cross_entropy_of_the_widest_rows(vrc, dtype, tokens, width):
+    say(f"{dtype} {tokens} x {width}")
+    check_entropy(vrc, tokens, [5, 0, 150], width, DT[dtype])
+    check_entropy_grad(vrc, tokens, [5, 0, 150], width, DT[dtype])
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("tokens", [2, 100, 130])
+def test_cross_entropy_of_the_largest_vocabulary(vrc, dtype, tokens):
+    vocab = [(1 << 23) - 301, 300] if tokens < 10 else [1 << 20, 300]
+    say(f"{dtype} {tokens} of {sum(vocab)}")
+    check_entropy(vrc, tokens, vocab, 8, DT[dtype])
+    check_entropy_grad(vrc, tokens, vocab, 8, DT[dtype])
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_cross_entropy_of_the_most_tokens(vrc, dtype):
+    say(dtype)
+    check_entropy(vrc, (1 << 24) - 1, [2, 1], 1, DT[dtype])
+    check_entropy_grad(vrc, (1 << 24) - 1, [2, 1], 1, DT[dtype], weighted=False, scale=1024.0)
+    torch.cuda.empty_cache()
+
+
+def test_calls_of_several_threads_at_once(vrc):
+    """Each thread on a stream and on data of its own; host code runs without the interpreter's lock."""
+    data = [inputs(110 + i, [torch.bfloat16, torch.float16, torch.float32][i % 3]) for i in range(4)]
+    want = [passes(vrc, d) for d in data]
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    got[i] = passes(vrc, data[i])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    same(want, got)
